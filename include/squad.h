@@ -281,6 +281,89 @@ squad_status squad_sp_unpack(const void* src, int ntensors, int slices, int rows
                              const int* counts, const int* src_rank, const int* src_row, void* const* dsts,
                              void* stream);
 
+/* ---- Rotary positions of the latent grid ----
+ * Queries and keys of a video transformer carry their token's place (t, y, x)
+ * as rotations (rotary position embedding; the pages leave positions to the
+ * model, gist.science technical summary, Methodology section 1). The rotated
+ * channels form pairs; pair i turns by the angle table[row(i, token)]:
+ *   y_a = x_a cos - x_b sin,   y_b = x_a sin + x_b cos.
+ * axes = (cT, cH, cW): channels of each axis (even, >= 0, sum r <= d). The first
+ * cT/2 pairs turn with t, the next cH/2 with y, the last cW/2 with x; channels
+ * r..d-1 are copied. Pair i is (2i, 2i+1) (SQUAD_ROTARY_ADJACENT) or
+ * (i, i + r/2) (SQUAD_ROTARY_HALF).
+ * table: device fp32 (cos, sin) pairs: T*cT/2 of them [t][pair], then H*cH/2
+ * [y][pair], then W*cW/2 [x][pair] (NULL where r = 0). Any angles may stand there, so an offset of
+ * the grid, a base or a rescaled position is a matter of the table. */
+typedef struct {
+  long long b, h, n; /* elements between batches, heads and tokens; channels are contiguous */
+} squad_strides;
+
+typedef enum { SQUAD_ROTARY_ADJACENT = 0, SQUAD_ROTARY_HALF = 1 } squad_rotary_pairing;
+
+typedef struct {
+  int B, d;        /* batch, head dimension */
+  int T, H, W;     /* latent grid, n = T*H*W tokens */
+  int cT, cH, cW;  /* channels turned by each axis */
+  int dtype;       /* squad_dtype of x and y */
+  int pairing;     /* squad_rotary_pairing */
+  int inverse;     /* nonzero: turn by the opposite angles (the gradient of the call without it) */
+} squad_rotary_desc;
+
+/* One launch over 1 or 2 tensors (queries and keys): y[i] = rotation of x[i], of
+ * heads[i] heads, with strides xs[i] and ys[i]. Every pointer and every stride (of
+ * an extent above 1) is a multiple of 16 bytes; y[i] may be x[i] with equal
+ * strides, else the tensors must not overlap. Products and sums in fp32, one
+ * rounding to the output. Limits (SQUAD_ERR_UNSUPPORTED): d a multiple of 16
+ * bytes, d <= 1024; SQUAD_ROTARY_HALF: r and d - r multiples of 32 bytes. */
+squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int* heads, const void* const* x,
+                          const squad_strides* xs, void* const* y, const squad_strides* ys, const float* table,
+                          void* stream);
+
+/* ---- Cross attention to an encoder's states ----
+ *   o = softmax(s * q K^T) V over the m states of the same batch row, for n
+ * queries: q, o [B, heads, n, d], k, v [B, kv_heads, m, d] with heads a multiple of
+ * kv_heads (query head i reads key head i / (heads/kv_heads)). n and m are free of
+ * each other. The layer of a video transformer that reads the prompt (the pages
+ * keep it as it is, gist.science technical summary, Methodology section 2).
+ * Masks (either, both or neither NULL): kv_lens [B] int32, keys at or past
+ * kv_lens[b] do not count (values below 0 mean 0, above m mean m); key_mask, one
+ * byte per key, mask_stride bytes between batch rows (0: one row for all), keys
+ * with a zero byte do not count. What k and v hold there does not matter, NaN and
+ * infinities included. A query whose keys are all masked gets o = 0, lse = -inf
+ * and gives no gradient.
+ * Tensors are strided (squad_strides, channels contiguous): token-major
+ * [B, n, heads, d] memory is as good as head-major. Pointers and strides (of
+ * extents above 1) are multiples of 16 bytes; batch and head strides of inputs may
+ * be 0 (broadcast). scale <= 0 selects 1/sqrt(d). lse [B, heads, n] fp32, contiguous.
+ * Limits (SQUAD_ERR_UNSUPPORTED): bf16 d in {64, 128}; f32 d a multiple of 32,
+ * d <= 256; B and heads <= 65535. */
+typedef struct {
+  int B, heads, kv_heads, n, m, d;
+  int dtype;                        /* squad_dtype */
+  float scale;
+  long long mask_stride;
+  squad_strides q, k, v, o;
+  squad_strides dout, dq, dk, dv;   /* read by squad_cross_bwd only */
+} squad_cross_desc;
+
+/* Device workspace: which = 0 for squad_cross_fwd (0 bytes where nothing is split
+ * over the keys), which = 1 for squad_cross_bwd. No CUDA call is made. */
+squad_status squad_cross_workspace_size(const squad_cross_desc* desc, int which, size_t* bytes);
+
+/* Forward. lse may be NULL (inference). workspace as above, 16-byte aligned,
+ * owned by the caller, overwritten, not shared with a call in flight. */
+squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
+                             const int* kv_lens, const unsigned char* key_mask, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward for the loss sum(o * dout): writes dq, dk and dv whole (zeros where
+ * nothing reaches). o and lse are the forward's. Gradients of shared key heads are
+ * summed over their query heads. Bitwise reproducible. */
+squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
+                             const int* kv_lens, const unsigned char* key_mask, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Geometry the kernels use for one pass (stage 1 = local/window pass,
  * stage 2 = global/cross-window pass), for tests and byte accounting.
  * Writes 8 ints to info: [0] rows per problem (w or m), [1] problems per

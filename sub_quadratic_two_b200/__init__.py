@@ -24,7 +24,8 @@ __all__ = [
     "poll_device_error", "library_path", "load_library", "SQUAD_F32", "SQUAD_BF16", "squad_attn_fwd_pass",
     "plan_info", "make_desc", "attention_multi", "squad_attn_multi_fwd", "squad_attn_multi_bwd",
     "multi_fwd_workspace_size", "attention_host",
-    "tmap_cache_stats",
+    "tmap_cache_stats", "cross_attention", "squad_cross_fwd", "squad_cross_bwd", "cross_workspace_size",
+    "Rotary", "rotary", "rotary_plan", "squad_rotary",
 ]
 
 SQUAD_F32 = 0
@@ -84,13 +85,18 @@ def load_library():
         lib.squad_poll_device_error.argtypes = [vp]
         ull = ctypes.POINTER(ctypes.c_ulonglong)
         lib.squad_tmap_cache_stats.argtypes = [ull, ull]
+        lib.squad_rotary.argtypes = [vp, ctypes.c_int, ip, vp, vp, vp, vp, vp, vp]
+        lib.squad_cross_workspace_size.argtypes = [vp, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+        lib.squad_cross_fwd.argtypes = [vp] * 9 + [sz, vp]
+        lib.squad_cross_bwd.argtypes = [vp] * 13 + [sz, vp]
         lib.squad_strerror.argtypes = [ctypes.c_int]
         lib.squad_strerror.restype = ctypes.c_char_p
         for f in ("squad_attn_workspace_size", "squad_attn_fwd", "squad_attn_bwd", "squad_poll_device_error",
                   "squad_attn_fwd_pass", "squad_plan_info", "squad_attn_fwd_host_workspace_size",
                   "squad_attn_fwd_host", "squad_attn_multi_fwd_workspace_size", "squad_attn_multi_fwd",
                   "squad_attn_multi_bwd_workspace_size", "squad_attn_multi_bwd",
-                  "squad_last_cuda_error", "squad_version", "squad_tmap_cache_stats"):
+                  "squad_last_cuda_error", "squad_version", "squad_tmap_cache_stats", "squad_rotary",
+                  "squad_cross_workspace_size", "squad_cross_fwd", "squad_cross_bwd"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -279,9 +285,23 @@ class _SquadAttention(torch.autograd.Function):
         return dq, dk, dv, None, None, None
 
 
+def _with_positions(q, k, grid, rot: Optional["Rotary"]):
+    """q and k turned by a rotary plan of the same grid (or as they are without one)."""
+    if rot is None:
+        return q, k
+    if tuple(rot.grid) != tuple(grid):
+        raise ValueError(f"the rotary plan is of grid {tuple(rot.grid)}, not {tuple(grid)}")
+    return _rotary_op(q, k, rot)
+
+
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grid: Tuple[int, int, int],
-              tile: Tuple[int, int, int], scale: Optional[float] = None) -> torch.Tensor:
-    """SQuad-Attention of [B, heads, T*H*W, d] CUDA tensors (float32 or bfloat16), differentiable."""
+              tile: Tuple[int, int, int], scale: Optional[float] = None,
+              rotary: Optional["Rotary"] = None) -> torch.Tensor:
+    """SQuad-Attention of [B, heads, T*H*W, d] CUDA tensors (float32 or bfloat16), differentiable.
+
+    rotary: a plan of the same grid (`rotary_plan`); q and k are turned by it first, and may then be strided.
+    """
+    q, k = _with_positions(q, k, grid, rotary)
     return _SquadAttention.apply(q, k, v, tuple(grid), tuple(tile), scale)
 
 
@@ -472,11 +492,21 @@ class _SquadAttentionMulti(torch.autograd.Function):
 
 
 def attention_multi(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grid: Tuple[int, int, int],
-                    tiles: Sequence[Tuple[int, int, int]], scale: Optional[float] = None) -> torch.Tensor:
+                    tiles: Sequence[Tuple[int, int, int]], scale: Optional[float] = None,
+                    rotary: Optional["Rotary"] = None) -> torch.Tensor:
     """k = len(tiles) + 1 passes over nested tiles (innermost first), differentiable.
 
     Pass j attends among the tokens of one t_j-window at the same position inside
     their t_{j-1}-window (t_0 = one token, the last window the whole grid); one
-    tile gives attention(q, k, v, grid, tiles[0]).
+    tile gives attention(q, k, v, grid, tiles[0]). rotary: as for `attention`.
     """
+    q, k = _with_positions(q, k, grid, rotary)
     return _SquadAttentionMulti.apply(q, k, v, tuple(grid), tuple(tuple(t) for t in tiles), scale)
+
+
+# ---------------------------------------------------------------- around the grid attention
+
+from .positions import Rotary, rotary, rotary_plan, squad_rotary  # noqa: E402
+from .cross import cross_attention, cross_workspace_size, squad_cross_bwd, squad_cross_fwd  # noqa: E402
+
+_rotary_op = rotary

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsquad.so")
-SOURCES = [os.path.join(CSRC, "squad_api.cu")]
+SOURCES = [os.path.join(CSRC, "squad_api.cu"), os.path.join(CSRC, "cross_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "squad.h")]
 
 
@@ -27,7 +27,7 @@ def nvcc() -> str:
 
 
 def command(out: str, ptxas_verbose: bool = False) -> list:
-    cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+    cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "--threads", "0",
            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC, "-o", out] + SOURCES
     if ptxas_verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -1,0 +1,155 @@
+"""Cross attention of the grid's tokens (or any queries) to an encoder's states of another length."""
+from __future__ import annotations
+
+import ctypes
+from functools import lru_cache
+from typing import Optional
+
+import torch
+
+from . import _check, _check_aux, _dtype_code, _ptr, _stream_handle, load_library
+from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout
+
+
+class SquadCrossDesc(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int) for f in ("B", "heads", "kv_heads", "n", "m", "d", "dtype")]
+                + [("scale", ctypes.c_float), ("mask_stride", ctypes.c_longlong)]
+                + [(f, SquadStrides) for f in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")])
+
+
+@lru_cache(maxsize=512)
+def _desc(q_shape, k_shape, code: int, scale: float, mask_stride: int, strides) -> SquadCrossDesc:
+    B, h, n, d = q_shape
+    desc = SquadCrossDesc(B, h, k_shape[1], n, k_shape[2], d, code, scale, mask_stride)
+    for name, st in zip(("q", "k", "v", "o", "dout", "dq", "dk", "dv"), strides):
+        setattr(desc, name, SquadStrides(*st[:3]))
+    return desc
+
+
+@lru_cache(maxsize=512)
+def _workspace(q_shape, k_shape, code: int, which: int) -> int:
+    nb = ctypes.c_size_t(0)
+    desc = _desc(q_shape, k_shape, code, 0.0, 0, ())
+    _check(load_library().squad_cross_workspace_size(ctypes.byref(desc), which, ctypes.byref(nb)),
+           "squad_cross_workspace_size")
+    return int(nb.value)
+
+
+def _check_cross(q, k, v, kv_lens, key_mask) -> int:
+    """Checks the operands; returns the key mask's batch stride in bytes."""
+    check_strided(("q", q), ("k", k), ("v", v))
+    B, h, _, d = q.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
+        raise ValueError("k and v must be [B, kv_heads, m, d] with q's batch and d")
+    if k.shape[1] == 0 or h % k.shape[1]:
+        raise ValueError(f"{h} query heads are not a multiple of {k.shape[1]} key heads")
+    if kv_lens is not None:
+        _check_aux(kv_lens, (B,), torch.int32, q.device, "kv_lens")
+    if key_mask is None:
+        return 0
+    m = k.shape[2]
+    if not isinstance(key_mask, torch.Tensor) or key_mask.device != q.device or key_mask.dtype != torch.bool:
+        raise ValueError(f"key_mask must be a bool tensor on {q.device}")
+    if tuple(key_mask.shape) not in ((B, m), (1, m)) or (m > 1 and key_mask.stride(1) != 1):
+        raise ValueError(f"key_mask must be [{B}, {m}] or [1, {m}] with contiguous rows")
+    step = 0 if key_mask.shape[0] == 1 else key_mask.stride(0)
+    if step != 0 and step < m:
+        raise ValueError("the rows of key_mask must not overlap")
+    return step
+
+
+def cross_workspace_size(q: torch.Tensor, k: torch.Tensor, which: int) -> int:
+    """Bytes of device workspace the forward (which = 0) or backward (1) of these shapes needs."""
+    return _workspace(tuple(q.shape), tuple(k.shape), _dtype_code(q), which)
+
+
+def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[torch.Tensor] = None,
+                    key_mask: Optional[torch.Tensor] = None, save: bool = True, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """Cross attention forward through the C ABI. Returns (o, lse); lse is None when save=False.
+
+    o lies in memory as q does (token-major or head-major), or in ``out``.
+    """
+    lib = load_library()
+    step = _check_cross(q, k, v, kv_lens, key_mask)
+    if out is not None:
+        check_strided(("q", q), ("out", out))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
+    o = empty_like_layout(q) if out is None else out
+    lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32) if save else None
+    if q.numel() == 0 or k.numel() == 0:  # no query, or no key for any of them
+        o.zero_()
+        if save:
+            lse.fill_(float("-inf"))
+        return o, lse
+    code = _dtype_code(q)
+    nb = _workspace(tuple(q.shape), tuple(k.shape), code, 0)
+    ws = torch.empty(nb, device=q.device, dtype=torch.uint8) if nb else None
+    desc = _desc(tuple(q.shape), tuple(k.shape), code, float(scale or 0.0), step,
+                 (q.stride(), k.stride(), v.stride(), o.stride()))
+    with torch.cuda.device(q.device):
+        _check(lib.squad_cross_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(key_mask),
+                                   _ptr(o), _ptr(lse), _ptr(ws), nb, _stream_handle(None, q.device)),
+               "squad_cross_fwd")
+    return o, lse
+
+
+def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_lens: Optional[torch.Tensor] = None,
+                    key_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Backward through the C ABI. Returns (dq, dk, dv), each lying in memory as q, k and v do."""
+    lib = load_library()
+    step = _check_cross(q, k, v, kv_lens, key_mask)
+    check_strided(("q", q), ("o", o), ("dout", dout))
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must have q's shape")
+    _check_aux(lse, q.shape[:3], torch.float32, q.device, "lse")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
+    dq, dk, dv = (empty_like_layout(t) for t in (q, k, v))
+    if q.numel() == 0 or k.numel() == 0:
+        return dq.zero_(), dk.zero_(), dv.zero_()
+    code = _dtype_code(q)
+    nb = _workspace(tuple(q.shape), tuple(k.shape), code, 1)
+    ws = torch.empty(nb, device=q.device, dtype=torch.uint8)
+    desc = _desc(tuple(q.shape), tuple(k.shape), code, float(scale or 0.0), step,
+                 tuple(t.stride() for t in (q, k, v, o, dout, dq, dk, dv)))
+    with torch.cuda.device(q.device):
+        _check(lib.squad_cross_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(key_mask),
+                                   _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), nb,
+                                   _stream_handle(None, q.device)), "squad_cross_bwd")
+    return dq, dk, dv
+
+
+class _CrossAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, scale, kv_lens, key_mask):
+        need = any(ctx.needs_input_grad[:3])
+        o, lse = squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save=need)
+        if need:
+            ctx.save_for_backward(q, k, v, o, lse, kv_lens, key_mask)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, o, lse, kv_lens, key_mask = ctx.saved_tensors
+        if not dense_enough(dout, dout.shape[3]):
+            dout = dout.contiguous()
+        return squad_cross_bwd(q, k, v, o, lse, dout, ctx.scale, kv_lens, key_mask) + (None, None, None)
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
+                    kv_lens: Optional[torch.Tensor] = None, key_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """softmax(scale * q k^T) v of queries [B, heads, n, d] over states [B, kv_heads, m, d], differentiable.
+
+    float32 or bfloat16 CUDA tensors, n and m free of each other, heads a multiple of kv_heads. Rows may be
+    strided (token-major [B, n, heads, d] memory seen through transpose(1, 2)); the output lies as q does.
+    kv_lens: [B] int32, the states of each batch row that count; key_mask: [B, m] (or [1, m]) bool, True
+    where a state counts. A query with no state left gets zeros and gives no gradient.
+    """
+    return _CrossAttention.apply(q, k, v, scale, kv_lens, key_mask)

@@ -1,0 +1,288 @@
+// cross_api.cu - C ABI of the operators around the grid attention: cross attention to an
+// encoder's states (squad_cross_*) and rotary positions (squad_rotary). Host side only:
+// argument checks, plans, tensor maps and launches on the caller's stream.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "squad.h"
+#include "cross_simt.cuh"
+#include "geometry.h"
+#include "host_state.h"
+#include "rotary.cuh"
+
+namespace {
+
+using sq::aligned16;
+
+#define SQ_CUDA(call)                                             \
+  do {                                                            \
+    cudaError_t e_ = (call);                                      \
+    if (e_ != cudaSuccess) return sq::host_cuda_fail(int(e_));    \
+  } while (0)
+
+constexpr long long kMaxRows = 1ll << 31;
+constexpr int kMaxGridYZ = 65535;
+
+size_t elem_size(int dtype) { return dtype == SQUAD_BF16 ? 2 : 4; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Strides a tensor of extents B x h x n may have: multiples of 16 bytes and not negative;
+// rows at least d apart, so that no two rows overlap; a stride of an extent of 1 is not
+// looked at. broadcast: batch and head strides of 0 are allowed (inputs).
+bool stride_ok(const squad_strides& s, int B, int h, int n, int d, size_t elem, bool broadcast) {
+  const long long unit = 16 / (long long)elem;
+  const long long lo = broadcast ? 0 : d;
+  if (n > 1 && (s.n < d || s.n % unit != 0 || s.n >= (1ll << 36))) return false;
+  if (h > 1 && (s.h < lo || s.h % unit != 0 || s.h >= (1ll << 36))) return false;
+  if (B > 1 && (s.b < lo || s.b % unit != 0 || s.b >= (1ll << 36))) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- cross attention
+
+squad_status check_cross(const squad_cross_desc* d) {
+  if (d == nullptr) return SQUAD_ERR_INVALID_ARG;
+  if (d->dtype != SQUAD_F32 && d->dtype != SQUAD_BF16) return SQUAD_ERR_INVALID_ARG;
+  if (!(d->scale > 0.f) && !(d->scale <= 0.f)) return SQUAD_ERR_INVALID_ARG;  // NaN
+  if (d->B <= 0 || d->heads <= 0 || d->kv_heads <= 0 || d->n <= 0 || d->m <= 0 || d->d <= 0) return SQUAD_ERR_SHAPE;
+  if (d->heads % d->kv_heads) return SQUAD_ERR_SHAPE;
+  const long long rows = (long long)d->B * d->heads, krows = (long long)d->B * d->kv_heads;
+  if (rows * d->n >= kMaxRows || krows * d->m >= kMaxRows) return SQUAD_ERR_SHAPE;
+  if (d->B > kMaxGridYZ || d->heads > kMaxGridYZ) return SQUAD_ERR_UNSUPPORTED;
+  if (d->dtype == SQUAD_BF16 ? (d->d != 64 && d->d != 128) : (d->d % 32 != 0 || d->d > 256))
+    return SQUAD_ERR_UNSUPPORTED;
+  return SQUAD_OK;
+}
+
+squad_status check_cross_strides(const squad_cross_desc* d, bool bwd) {
+  const size_t e = elem_size(d->dtype);
+  const int B = d->B, h = d->heads, hk = d->kv_heads;
+  if (!stride_ok(d->q, B, h, d->n, d->d, e, true) || !stride_ok(d->k, B, hk, d->m, d->d, e, true) ||
+      !stride_ok(d->v, B, hk, d->m, d->d, e, true) || !stride_ok(d->o, B, h, d->n, d->d, e, false))
+    return SQUAD_ERR_ALIGN;
+  if (bwd && (!stride_ok(d->dout, B, h, d->n, d->d, e, true) || !stride_ok(d->dq, B, h, d->n, d->d, e, false) ||
+              !stride_ok(d->dk, B, hk, d->m, d->d, e, false) || !stride_ok(d->dv, B, hk, d->m, d->d, e, false)))
+    return SQUAD_ERR_ALIGN;
+  return SQUAD_OK;
+}
+
+sq::CrossStride strides_of(const squad_strides& s) { return {s.b, s.h, s.n}; }
+
+size_t bwd_rowvec_bytes(const squad_cross_desc* d) { return align256(size_t(d->B) * d->heads * d->n * sizeof(float)); }
+
+sq::CrossArgs cross_args(const squad_cross_desc* d, const void* q, const void* k, const void* v, const int* kv_lens,
+                         const unsigned char* key_mask) {
+  sq::CrossArgs a{};
+  a.B = d->B;
+  a.heads = d->heads;
+  a.kv_heads = d->kv_heads;
+  a.group = d->heads / d->kv_heads;
+  a.n = d->n;
+  a.m = d->m;
+  a.d = d->d;
+  a.scale = d->scale > 0.f ? d->scale : 1.0f / std::sqrt(float(d->d));
+  a.mask = {kv_lens, key_mask, d->mask_stride};
+  a.sq = strides_of(d->q);
+  a.sk = strides_of(d->k);
+  a.sv = strides_of(d->v);
+  a.so = strides_of(d->o);
+  a.sdo = strides_of(d->dout);
+  a.sdq = strides_of(d->dq);
+  a.sdk = strides_of(d->dk);
+  a.sdv = strides_of(d->dv);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  return a;
+}
+
+dim3 row_grid(const sq::CrossArgs& a, int rows, int heads) {
+  return dim3(unsigned((rows + sq::kSimtWarps - 1) / sq::kSimtWarps), unsigned(heads), unsigned(a.B));
+}
+
+template <typename T, int DPL>
+squad_status simt_cross_fwd(const sq::CrossArgs& a, cudaStream_t st) {
+  sq::cross_simt_fwd_kernel<T, DPL><<<row_grid(a, a.n, a.heads), sq::kSimtWarps * 32, 0, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
+template <typename T, int DPL>
+squad_status simt_cross_bwd(const sq::CrossArgs& a, cudaStream_t st) {
+  sq::cross_simt_dq_kernel<T, DPL><<<row_grid(a, a.n, a.heads), sq::kSimtWarps * 32, 0, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  sq::cross_simt_dkdv_kernel<T, DPL><<<row_grid(a, a.m, a.kv_heads), sq::kSimtWarps * 32, 0, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
+template <typename T, bool BWD>
+squad_status simt_cross(const sq::CrossArgs& a, cudaStream_t st) {
+#define SQ_DPL(N) \
+  case N:         \
+    return BWD ? simt_cross_bwd<T, N>(a, st) : simt_cross_fwd<T, N>(a, st)
+  switch (a.d / 32) {
+    SQ_DPL(1);
+    SQ_DPL(2);
+    SQ_DPL(3);
+    SQ_DPL(4);
+    SQ_DPL(5);
+    SQ_DPL(6);
+    SQ_DPL(7);
+    SQ_DPL(8);
+  }
+#undef SQ_DPL
+  return SQUAD_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+squad_status squad_cross_workspace_size(const squad_cross_desc* desc, int which, size_t* bytes) {
+  if (bytes == nullptr) return SQUAD_ERR_INVALID_ARG;
+  squad_status s = check_cross(desc);
+  if (s != SQUAD_OK) return s;
+  if (which == 0)
+    *bytes = 0;
+  else if (which == 1)
+    *bytes = bwd_rowvec_bytes(desc);
+  else
+    return SQUAD_ERR_INVALID_ARG;
+  return SQUAD_OK;
+}
+
+squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
+                             const int* kv_lens, const unsigned char* key_mask, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  squad_status s = squad_cross_workspace_size(desc, 0, &need);
+  if (s != SQUAD_OK) return s;
+  if (q == nullptr || k == nullptr || v == nullptr || o == nullptr) return SQUAD_ERR_INVALID_ARG;
+  if (key_mask != nullptr && desc->mask_stride != 0 && desc->mask_stride < desc->m) return SQUAD_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(p)) return SQUAD_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(kv_lens) & 3u) return SQUAD_ERR_ALIGN;
+  if ((s = check_cross_strides(desc, false)) != SQUAD_OK) return s;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SQUAD_ERR_WORKSPACE;
+  sq::HostDevice dev;
+  if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
+  sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
+  a.o = o;
+  a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return desc->dtype == SQUAD_BF16 ? simt_cross<__nv_bfloat16, false>(a, st) : simt_cross<float, false>(a, st);
+}
+
+squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
+                             const int* kv_lens, const unsigned char* key_mask, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  squad_status s = squad_cross_workspace_size(desc, 1, &need);
+  if (s != SQUAD_OK) return s;
+  for (const void* p : {q, k, v, o, static_cast<const void*>(lse), dout, static_cast<const void*>(dq),
+                        static_cast<const void*>(dk), static_cast<const void*>(dv)}) {
+    if (p == nullptr) return SQUAD_ERR_INVALID_ARG;
+    if (!aligned16(p)) return SQUAD_ERR_ALIGN;
+  }
+  if (key_mask != nullptr && desc->mask_stride != 0 && desc->mask_stride < desc->m) return SQUAD_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u)) return SQUAD_ERR_ALIGN;
+  if ((s = check_cross_strides(desc, true)) != SQUAD_OK) return s;
+  if (workspace == nullptr || workspace_bytes < need) return SQUAD_ERR_WORKSPACE;
+  sq::HostDevice dev;
+  if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
+  sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
+  a.o_in = o;
+  a.lse = const_cast<float*>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.Drow = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return desc->dtype == SQUAD_BF16 ? simt_cross<__nv_bfloat16, true>(a, st) : simt_cross<float, true>(a, st);
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int* heads, const void* const* x,
+                          const squad_strides* xs, void* const* y, const squad_strides* ys, const float* table,
+                          void* stream) {
+  if (desc == nullptr || heads == nullptr || x == nullptr || xs == nullptr || y == nullptr || ys == nullptr ||
+      ntensors < 1 || ntensors > 2)
+    return SQUAD_ERR_INVALID_ARG;
+  const squad_rotary_desc& d = *desc;
+  if (d.dtype != SQUAD_F32 && d.dtype != SQUAD_BF16) return SQUAD_ERR_INVALID_ARG;
+  if (d.pairing != SQUAD_ROTARY_ADJACENT && d.pairing != SQUAD_ROTARY_HALF) return SQUAD_ERR_INVALID_ARG;
+  if (d.B <= 0 || d.d <= 0 || d.T <= 0 || d.H <= 0 || d.W <= 0) return SQUAD_ERR_SHAPE;
+  if (d.cT < 0 || d.cH < 0 || d.cW < 0 || (d.cT | d.cH | d.cW) % 2) return SQUAD_ERR_SHAPE;
+  if ((long long)d.cT + d.cH + d.cW > d.d) return SQUAD_ERR_SHAPE;
+  const size_t e = elem_size(d.dtype);
+  const int per = int(16 / e);  // channels of a 16-byte chunk
+  const int r = d.cT + d.cH + d.cW;
+  const bool half = d.pairing == SQUAD_ROTARY_HALF;
+  if (d.d % per || d.d > 1024 || (half && (r % (2 * per) || (d.d - r) % (2 * per)))) return SQUAD_ERR_UNSUPPORTED;
+  const long long n = (long long)d.T * d.H * d.W;
+  if (n >= kMaxRows) return SQUAD_ERR_SHAPE;
+  if (d.B > kMaxGridYZ) return SQUAD_ERR_UNSUPPORTED;
+  const long long entries[3] = {(long long)d.T * (d.cT / 2), (long long)d.H * (d.cH / 2), (long long)d.W * (d.cW / 2)};
+  if (entries[0] + entries[1] + entries[2] >= kMaxRows) return SQUAD_ERR_SHAPE;
+  if (table == nullptr && r > 0) return SQUAD_ERR_INVALID_ARG;
+  sq::RotaryArgs a{};
+  long long total = 0;
+  for (int i = 0; i < ntensors; ++i) {
+    if (heads[i] <= 0) return SQUAD_ERR_SHAPE;
+    if (x[i] == nullptr || y[i] == nullptr) return SQUAD_ERR_INVALID_ARG;
+    if (!aligned16(x[i]) || !aligned16(y[i])) return SQUAD_ERR_ALIGN;
+    if (!stride_ok(xs[i], d.B, heads[i], int(n), d.d, e, true) || !stride_ok(ys[i], d.B, heads[i], int(n), d.d, e, false))
+      return SQUAD_ERR_ALIGN;
+    total += heads[i];
+    const long long es = (long long)e;
+    a.t[i] = {static_cast<const uint8_t*>(x[i]), static_cast<uint8_t*>(y[i]), xs[i].b * es, xs[i].h * es,
+              xs[i].n * es, ys[i].b * es, ys[i].h * es, ys[i].n * es, heads[i]};
+  }
+  if (reinterpret_cast<uintptr_t>(table) & 7u) return SQUAD_ERR_ALIGN;
+  const long long groups = (total + sq::kRotaryHeads - 1) / sq::kRotaryHeads;
+  if (groups > kMaxGridYZ) return SQUAD_ERR_UNSUPPORTED;
+  a.table = reinterpret_cast<const float2*>(table);
+  a.n = int(n);
+  a.W = d.W;
+  a.H = d.H;
+  a.pT = d.cT / 2;
+  a.pH = d.cH / 2;
+  a.pW = d.cW / 2;
+  a.offH = int(entries[0]);
+  a.offW = int(entries[0] + entries[1]);
+  a.lanes = d.d / (half ? 2 * per : per);
+  a.rows = sq::kRotaryThreads / a.lanes;
+  a.f_lanes = sq::make_fastdiv(uint32_t(a.lanes));
+  a.f_w = sq::make_fastdiv(uint32_t(d.W));
+  a.f_h = sq::make_fastdiv(uint32_t(d.H));
+  a.sign = d.inverse ? -1.f : 1.f;
+  sq::HostDevice dev;
+  squad_status s = sq::host_device(&dev);
+  if (s != SQUAD_OK) return s;
+  const dim3 grid(unsigned((n + a.rows - 1) / a.rows), unsigned(groups), unsigned(d.B));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d.dtype == SQUAD_BF16) {
+    if (half)
+      sq::rotary_kernel<__nv_bfloat16, true><<<grid, sq::kRotaryThreads, 0, st>>>(a);
+    else
+      sq::rotary_kernel<__nv_bfloat16, false><<<grid, sq::kRotaryThreads, 0, st>>>(a);
+  } else {
+    if (half)
+      sq::rotary_kernel<float, true><<<grid, sq::kRotaryThreads, 0, st>>>(a);
+    else
+      sq::rotary_kernel<float, false><<<grid, sq::kRotaryThreads, 0, st>>>(a);
+  }
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
+}  // extern "C"

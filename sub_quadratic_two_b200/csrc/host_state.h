@@ -1,0 +1,34 @@
+// host_state.h - host-side state and helpers shared by the library's translation units
+// (defined in squad_api.cu): per-device facts, the error word, tensor-map encoding.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "squad.h"
+
+#define SQ_HIDDEN __attribute__((visibility("hidden")))
+
+namespace sq {
+
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
+
+struct HostDevice {
+  int device;
+  int sms;
+  int* err;  // device address of the library's error word
+};
+
+// Facts of the current device; binds its primary context to this thread.
+SQ_HIDDEN squad_status host_device(HostDevice* out);
+// Remembers a failing CUDA call's code for squad_last_cuda_error.
+SQ_HIDDEN squad_status host_cuda_fail(int code);
+// Tiled bf16 tensor map with the 128-byte swizzle (taken from the cache where it was made
+// before); call host_device first.
+SQ_HIDDEN squad_status host_encode_bf16(CUtensorMap* m, int device, int rank, const void* base,
+                                        const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace sq

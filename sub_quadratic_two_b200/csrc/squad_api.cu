@@ -14,6 +14,7 @@
 
 #include "squad.h"
 #include "geometry.h"
+#include "host_state.h"
 #include "squad_bwd_fused.cuh"
 #include "squad_fwd_tc.cuh"
 #include "squad_simt.cuh"
@@ -27,7 +28,7 @@ using sq::Geom;
 
 constexpr int kVersion = 1 * 10000 + 0 * 100 + 0;
 constexpr int kMaxDevices = 64;
-constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
+using sq::kWaitTimeoutNs;
 constexpr int kFusedLag = 2;  // heads between a local pass and its global pass (see decode_item)
 constexpr int kMultiLag = 2;  // heads between pass j-1 and pass j of a head in the k-pass launch
 
@@ -102,7 +103,7 @@ struct Plan {
   float scale;
 };
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using sq::aligned16;
 
 // with_passes = false checks the tensors only (the k-pass entry points plan their own passes)
 squad_status make_plan(const squad_desc* d, Plan* p, bool with_passes = true) {
@@ -164,27 +165,32 @@ BwdWs bwd_workspace(const Plan& p, const squad_desc* d) {
 // Encoded maps are reused by later calls with the same pointers and shapes (tmap_cache.h).
 sq::TmapCache<128> g_tmaps;
 
-squad_status encode_map(CUtensorMap* m, const void* base, const Geom& g, int d, long long rows) {
-  const cuuint64_t esz = 2;
-  // a packed dimension spans the packed digit's full extent (its rows past that extent read as zeros)
-  cuuint64_t dims[5] = {cuuint64_t(d), cuuint64_t(g.pk_dim == 0 ? g.pk_ext : g.a_n),
-                        cuuint64_t(g.pk_dim == 1 ? g.pk_ext : g.b_n), cuuint64_t(g.pk_dim == 2 ? g.pk_ext : g.c_n),
-                        cuuint64_t(rows)};
-  cuuint64_t strides[4] = {cuuint64_t(g.sA) * d * esz, cuuint64_t(g.sB) * d * esz, cuuint64_t(g.sC) * d * esz,
-                           cuuint64_t(d) * esz};
-  cuuint32_t box[5] = {64u, cuuint32_t(g.a_n), cuuint32_t(g.b_sub), cuuint32_t(g.c_sub), 1u};
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  int dev = 0;
-  SQ_CUDA(cudaGetDevice(&dev));
-  const sq::TmapKey key = sq::make_tmap_key(dev, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, 5, base,
-                                            dims, strides, box);
+squad_status encode_tiled(CUtensorMap* m, int dev, int rank, const void* base, const uint64_t* dims,
+                          const uint64_t* strides, const uint32_t* box) {
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const sq::TmapKey key = sq::make_tmap_key(dev, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, rank,
+                                            base, dims, strides, box);
   CUresult r = g_tmaps.get(key, m, [&](CUtensorMap* out) {
-    return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   });
   if (r != CUDA_SUCCESS) return cuda_fail(int(r));
   return SQUAD_OK;
+}
+
+squad_status encode_map(CUtensorMap* m, const void* base, const Geom& g, int d, long long rows) {
+  const cuuint64_t esz = 2;
+  // a packed dimension spans the packed digit's full extent (its rows past that extent read as zeros)
+  uint64_t dims[5] = {cuuint64_t(d), cuuint64_t(g.pk_dim == 0 ? g.pk_ext : g.a_n),
+                        cuuint64_t(g.pk_dim == 1 ? g.pk_ext : g.b_n), cuuint64_t(g.pk_dim == 2 ? g.pk_ext : g.c_n),
+                        cuuint64_t(rows)};
+  uint64_t strides[4] = {cuuint64_t(g.sA) * d * esz, cuuint64_t(g.sB) * d * esz, cuuint64_t(g.sC) * d * esz,
+                           cuuint64_t(d) * esz};
+  uint32_t box[5] = {64u, cuuint32_t(g.a_n), cuuint32_t(g.b_sub), cuuint32_t(g.c_sub), 1u};
+  int dev = 0;
+  SQ_CUDA(cudaGetDevice(&dev));
+  return encode_tiled(m, dev, 5, base, dims, strides, box);
 }
 
 // ---------------------------------------------------------------- launches
@@ -472,6 +478,27 @@ squad_status simt_bwd(const Plan& p, const BwdWs& w, uint8_t* ws, const void* q,
 }
 
 }  // namespace
+
+namespace sq {
+
+squad_status host_device(HostDevice* out) {
+  DeviceState* ds = nullptr;
+  squad_status s = device_state(&ds);
+  if (s != SQUAD_OK) return s;
+  out->device = int(ds - g_dev);
+  out->sms = ds->sms;
+  out->err = ds->err;
+  return SQUAD_OK;
+}
+
+squad_status host_cuda_fail(int code) { return cuda_fail(code); }
+
+squad_status host_encode_bf16(CUtensorMap* m, int device, int rank, const void* base, const uint64_t* dims,
+                              const uint64_t* strides, const uint32_t* box) {
+  return encode_tiled(m, device, rank, base, dims, strides, box);
+}
+
+}  // namespace sq
 
 // One thread waits on a barrier that nothing completes: the bounded wait gives up
 // after timeout_ns and the error word is set (the test of the device timeout path).

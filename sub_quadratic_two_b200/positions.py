@@ -1,0 +1,204 @@
+"""Rotary positions of the latent grid: the angles of a token's (t, y, x), applied to queries and keys.
+
+`rotary_plan` makes the table of a grid, `rotary` turns [B, heads, T*H*W, d] tensors by it (differentiable;
+strided inputs such as a projection's token-major output come out contiguous, as `attention` takes them),
+and `attention` and `attention_multi` take a plan as `rotary=`.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from functools import lru_cache
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import _check, _dtype_code, _ptr, _stream_handle, load_library
+
+PAIRINGS = {"adjacent": 0, "half": 1}
+
+
+class SquadStrides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("n", ctypes.c_longlong)]
+
+
+class SquadRotaryDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("B", "d", "T", "H", "W", "cT", "cH", "cW", "dtype", "pairing", "inverse")]
+
+
+def strides_of(t: torch.Tensor) -> SquadStrides:
+    return SquadStrides(*t.stride()[:3])
+
+
+def token_major(t: torch.Tensor) -> bool:
+    """Whether a [B, heads, n, d] tensor lies in memory as [B, n, heads, d]."""
+    return t.shape[1] > 1 and t.shape[2] > 1 and t.stride(1) < t.stride(2)
+
+
+def empty_like_layout(t: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of t's shape, token-major where t is, else head-major."""
+    B, h, n, d = t.shape
+    if token_major(t):
+        return torch.empty((B, n, h, d), device=t.device, dtype=t.dtype).transpose(1, 2)
+    return torch.empty((B, h, n, d), device=t.device, dtype=t.dtype)
+
+
+def check_strided(*named):
+    """(name, tensor) pairs: CUDA tensors [B, heads, rows, d] of one dtype and device, channels contiguous."""
+    ref = named[0][1]
+    for name, t in named:
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, heads, rows, d] tensor")
+        if not t.is_cuda:
+            raise ValueError("libsquad needs CUDA tensors (there is no CPU path)")
+        if t.dtype != ref.dtype or t.device != ref.device:
+            raise ValueError(f"{name} must share {named[0][0]}'s dtype and device")
+        if t.shape[3] > 1 and t.stride(3) != 1 and t.numel() > 0:
+            raise ValueError(f"the channels of {name} must be contiguous (stride 1 along d)")
+    _dtype_code(ref)
+
+
+def dense_enough(t: torch.Tensor, rows_apart: int) -> bool:
+    """Whether the kernels take a gradient as it lies: channels contiguous, rows apart, 16-byte steps."""
+    unit = 16 // t.element_size()
+    if t.data_ptr() % 16 or (t.shape[3] > 1 and t.stride(3) != 1):
+        return False
+    return all(size <= 1 or (step >= rows_apart and step % unit == 0) for size, step in zip(t.shape[:3], t.stride()[:3]))
+
+
+def default_axes(d: int) -> Tuple[int, int, int]:
+    """Channels of (time, height, width): height and width a third each in whole pairs, time the rest."""
+    side = 2 * (d // 6)
+    return d - 2 * side, side, side
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """The rotation of a T x H x W grid.
+
+    axes: channels turned by time, height and width (even, their sum at most d; channels past it are copied).
+    table: [T*axes[0]/2 + H*axes[1]/2 + W*axes[2]/2, 2] float32 CUDA tensor of (cos, sin): per axis one row
+    of pairs for each position. pairing: "adjacent" turns channels (2i, 2i+1), "half" (i, i + sum(axes)/2).
+    """
+    grid: Tuple[int, int, int]
+    axes: Tuple[int, int, int]
+    table: torch.Tensor
+    pairing: str = "adjacent"
+
+    def __post_init__(self):
+        if len(self.grid) != 3 or len(self.axes) != 3 or min(self.grid) < 1 or min(self.axes) < 0:
+            raise ValueError("grid and axes are (time, height, width): positive sizes, channels of each")
+        if any(c % 2 for c in self.axes):
+            raise ValueError("axes must be even: channels turn in pairs")
+        if self.pairing not in PAIRINGS:
+            raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
+        t = self.table
+        rows = sum(size * (c // 2) for size, c in zip(self.grid, self.axes))
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (rows, 2):
+            raise ValueError(f"table must be float32 of shape {(rows, 2)}")
+        if not t.is_contiguous():
+            raise ValueError("table must be contiguous")
+
+
+def rotary_plan(grid: Sequence[int], d: int, axes: Optional[Sequence[int]] = None, theta: float = 10000.0,
+                offset: Sequence[float] = (0, 0, 0), pairing: str = "adjacent", device=None) -> Rotary:
+    """The plan of a grid: pair i of an axis with c channels at position p turns by (offset + p) * theta^(-2i/c).
+
+    offset: the position of the grid's first token (a later frame of a stream, a rank's first frame).
+    Angles are taken in float64 on the host, so that far positions keep their accuracy.
+    """
+    grid = tuple(int(x) for x in grid)
+    axes = default_axes(int(d)) if axes is None else tuple(int(c) for c in axes)
+    if sum(axes) > d:
+        raise ValueError(f"axes {axes} turn more than d={d} channels")
+    if len(offset) != 3:
+        raise ValueError("offset is (time, height, width)")
+    parts = []
+    for size, c, first in zip(grid, axes, offset):
+        freq = float(theta) ** (-torch.arange(0, c, 2, dtype=torch.float64) / max(c, 1))
+        ang = (torch.arange(size, dtype=torch.float64) + float(first))[:, None] * freq
+        parts.append(torch.stack([ang.cos(), ang.sin()], -1).reshape(-1, 2))
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return Rotary(grid, axes, torch.cat(parts).float().contiguous().to(dev), pairing)
+
+
+@lru_cache(maxsize=256)
+def _rotary_desc(B: int, d: int, grid, axes, code: int, pairing: str, inverse: bool) -> SquadRotaryDesc:
+    return SquadRotaryDesc(B, d, *grid, *axes, code, PAIRINGS[pairing], int(inverse))
+
+
+def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
+                 out: Optional[Sequence[torch.Tensor]] = None, stream: Optional[torch.cuda.Stream] = None):
+    """One or two tensors [B, heads, T*H*W, d] through the C ABI in one launch; returns the list of outputs.
+
+    inverse turns by the opposite angles. out: tensors to write (any strides of whole 16-byte steps; an input
+    itself for the rotation in place), else contiguous ones are made.
+    """
+    lib = load_library()
+    check_strided(*[(f"xs[{i}]", x) for i, x in enumerate(xs)])
+    if not 1 <= len(xs) <= 2:
+        raise ValueError("one or two tensors")
+    ref = xs[0]
+    B, _, n, d = ref.shape
+    T, H, W = rot.grid
+    for x in xs:
+        if (x.shape[0], x.shape[2], x.shape[3]) != (B, n, d):
+            raise ValueError("the tensors must share batch, tokens and d")
+    if n != T * H * W:
+        raise ValueError(f"n={n} but T*H*W={T * H * W}")
+    if rot.table.device != ref.device:
+        raise ValueError(f"the rotary table must be on {ref.device}")
+    if out is not None:
+        check_strided(("xs[0]", ref), *[(f"out[{i}]", y) for i, y in enumerate(out)])
+        if len(out) != len(xs) or any(x.shape != y.shape for x, y in zip(xs, out)):
+            raise ValueError("out must hold one tensor of each input's shape")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return squad_rotary(xs, rot, inverse, out)
+    ys = [torch.empty(x.shape, device=x.device, dtype=x.dtype) for x in xs] if out is None else list(out)
+    if B == 0 or any(x.shape[1] == 0 for x in xs):
+        return ys
+    c = len(xs)
+    desc = _rotary_desc(B, d, tuple(rot.grid), tuple(rot.axes), _dtype_code(ref), rot.pairing, bool(inverse))
+    with torch.cuda.device(ref.device):
+        _check(lib.squad_rotary(ctypes.byref(desc), c, (ctypes.c_int * c)(*[x.shape[1] for x in xs]),
+                                (ctypes.c_void_p * c)(*[x.data_ptr() for x in xs]),
+                                (SquadStrides * c)(*[strides_of(x) for x in xs]),
+                                (ctypes.c_void_p * c)(*[y.data_ptr() for y in ys]),
+                                (SquadStrides * c)(*[strides_of(y) for y in ys]), _ptr(rot.table),
+                                _stream_handle(None, ref.device)), "squad_rotary")
+    return ys
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rot, *xs):
+        ctx.rot = rot
+        ctx.token_major = [token_major(x) for x in xs]
+        return tuple(squad_rotary(xs, rot))
+
+    @staticmethod
+    def backward(ctx, *grads):
+        out = [None] * len(grads)
+        take = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[1 + i]]
+        if take:
+            gs = [grads[i] if dense_enough(grads[i], grads[i].shape[3]) else grads[i].contiguous() for i in take]
+            ys = []
+            for i, g in zip(take, gs):
+                B, h, n, d = g.shape
+                y = torch.empty((B, n, h, d) if ctx.token_major[i] else (B, h, n, d), device=g.device, dtype=g.dtype)
+                ys.append(y.transpose(1, 2) if ctx.token_major[i] else y)
+            for i, y in zip(take, squad_rotary(gs, ctx.rot, inverse=True, out=ys)):
+                out[i] = y
+        return (None, *out)
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary):
+    """(q, k) turned by the grid's positions, as contiguous [B, heads, T*H*W, d] tensors (float32 or bfloat16).
+
+    k may have its own number of heads, or be None (then None comes back in its place). Differentiable; the
+    gradients come in the memory layout of q and k.
+    """
+    if k is None:
+        return _Rotary.apply(rot, q)[0], None
+    return _Rotary.apply(rot, q, k)
