@@ -5,10 +5,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "squad.h"
+#include "cross_fwd_tc.cuh"
 #include "cross_simt.cuh"
 #include "geometry.h"
 #include "host_state.h"
@@ -139,6 +141,106 @@ squad_status simt_cross(const sq::CrossArgs& a, cudaStream_t st) {
   return SQUAD_ERR_UNSUPPORTED;
 }
 
+// ---------------------------------------------------------------- tensor-core forward (bf16)
+
+// 4-D map (channel, row, head, batch) over a strided tensor, boxes of 64 channels x 128 rows.
+// Extents that are 1 or broadcast (stride 0) are left out: their coordinate is times mb, mh.
+squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void* base, const squad_strides& st, int B,
+                         int h, int n, int d, int* mb, int* mh) {
+  const uint64_t row = uint64_t(d) * 2;
+  *mb = B > 1 && st.b != 0;
+  *mh = h > 1 && st.h != 0;
+  const uint64_t dims[4] = {uint64_t(d), uint64_t(n), *mh ? uint64_t(h) : 1, *mb ? uint64_t(B) : 1};
+  const uint64_t strides[3] = {n > 1 ? uint64_t(st.n) * 2 : row, *mh ? uint64_t(st.h) * 2 : row,
+                               *mb ? uint64_t(st.b) * 2 : row};
+  const uint32_t box[4] = {64, 128, 1, 1};
+  return sq::host_encode_bf16(map, dev.device, 4, base, dims, strides, box);
+}
+
+constexpr int kMaxDevices = 64;
+
+// The attribute is set once per kernel and device; a repeated set by two threads is harmless.
+template <typename K>
+squad_status allow_smem(K kern, int bytes, const sq::HostDevice& dev, std::atomic<bool>* done) {
+  if (!done[dev.device].load(std::memory_order_acquire)) {
+    SQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done[dev.device].store(true, std::memory_order_release);
+  }
+  return SQUAD_OK;
+}
+
+struct FwdWs {
+  size_t part_o, part_lse, total;
+};
+
+FwdWs fwd_workspace(const squad_cross_desc* d) {
+  FwdWs w{};
+  if (d->dtype != SQUAD_BF16) return w;
+  const sq::CrossPlan p = sq::make_cross_plan(d->B, d->heads, d->kv_heads, d->n, d->m);
+  if (p.splits <= 1) return w;
+  const size_t rows = size_t(d->B) * d->heads * d->n * p.splits;
+  w.part_lse = align256(rows * d->d * sizeof(float));
+  w.total = w.part_lse + align256(rows * sizeof(float));
+  return w;
+}
+
+template <int D, bool MASKED>
+squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& maps, const sq::CrossFwdArgs& a,
+                              cudaStream_t st) {
+  using Lay = sq::CrossFwdLayout<D>;
+  auto kern = sq::cross_fwd_tc_kernel<D, MASKED>;
+  static std::atomic<bool> done[kMaxDevices];
+  squad_status s = allow_smem(kern, Lay::BYTES, dev, done);
+  if (s != SQUAD_OK) return s;
+  const int grid = a.plan.items < dev.sms ? a.plan.items : dev.sms;
+  kern<<<grid, sq::kCrossThreads, Lay::BYTES, st>>>(maps, a);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
+squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c, void* ws,
+                          cudaStream_t st) {
+  sq::CrossMaps maps;
+  sq::CrossFwdArgs a{};
+  a.plan = sq::make_cross_plan(d->B, d->heads, d->kv_heads, d->n, d->m);
+  a.B = d->B;
+  a.heads = d->heads;
+  a.n = d->n;
+  a.m = d->m;
+  squad_status s;
+  if ((s = encode_rows(&maps.q, dev, c.q, d->q, d->B, d->heads, d->n, d->d, &a.q_b, &a.q_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.k, dev, c.k, d->k, d->B, d->kv_heads, d->m, d->d, &a.k_b, &a.k_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.v, dev, c.v, d->v, d->B, d->kv_heads, d->m, d->d, &a.v_b, &a.v_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.o, dev, c.o, d->o, d->B, d->heads, d->n, d->d, &a.o_b, &a.o_h)) != SQUAD_OK) return s;
+  a.mask = c.mask;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  a.lse = c.lse;
+  a.err = dev.err;
+  a.timeout_ns = sq::kWaitTimeoutNs;
+  const FwdWs w = fwd_workspace(d);
+  if (a.plan.splits > 1) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part_lse);
+  }
+  const bool masked = c.mask.lens != nullptr || c.mask.keys != nullptr;
+  if (d->d == 128)
+    s = masked ? launch_cross_fwd<128, true>(dev, maps, a, st) : launch_cross_fwd<128, false>(dev, maps, a, st);
+  else
+    s = masked ? launch_cross_fwd<64, true>(dev, maps, a, st) : launch_cross_fwd<64, false>(dev, maps, a, st);
+  if (s != SQUAD_OK || a.plan.splits <= 1) return s;
+  const long long rows = (long long)d->B * d->heads * d->n;
+  const unsigned blocks = unsigned((rows + 3) / 4);
+  auto* o = static_cast<__nv_bfloat16*>(c.o);
+  if (d->d == 128)
+    sq::cross_join_kernel<128><<<blocks, 128, 0, st>>>(a.part_o, a.part_lse, a.plan.splits, rows, d->heads, d->n, o,
+                                                       c.so, c.lse);
+  else
+    sq::cross_join_kernel<64><<<blocks, 128, 0, st>>>(a.part_o, a.part_lse, a.plan.splits, rows, d->heads, d->n, o,
+                                                      c.so, c.lse);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,7 +250,7 @@ squad_status squad_cross_workspace_size(const squad_cross_desc* desc, int which,
   squad_status s = check_cross(desc);
   if (s != SQUAD_OK) return s;
   if (which == 0)
-    *bytes = 0;
+    *bytes = fwd_workspace(desc).total;
   else if (which == 1)
     *bytes = bwd_rowvec_bytes(desc);
   else
@@ -176,7 +278,7 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
   a.o = o;
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? simt_cross<__nv_bfloat16, false>(a, st) : simt_cross<float, false>(a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, workspace, st) : simt_cross<float, false>(a, st);
 }
 
 squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,

@@ -1,0 +1,99 @@
+// cross_plan.h - how a cross-attention forward is cut into work (host and device code).
+//
+// A job is one 128-query tile over a range of 128-key blocks; an item is two jobs of one
+// (batch, head), run side by side on one SM. Where the query tiles fill the SMs, the jobs of
+// an item are two neighbouring tiles over all keys, which share the key and value tiles in
+// shared memory. Where they do not, an item takes one tile alone (a second SM is better than
+// a shared tile), and where even that leaves SMs idle the keys of a tile are split over
+// `splits` jobs, whose partial results a second kernel joins.
+#pragma once
+#include <cstdint>
+#include "geometry.h"
+
+namespace sq {
+
+constexpr int kCrossPlanSms = 148;  // the plan depends on sizes alone, so that results do too
+
+struct CrossPlan {
+  int qtiles;       // 128-row query tiles per (batch, head)
+  int kblocks;      // 128-key blocks of m
+  int tiles;        // query tiles per item: 2 (sharing keys) or 1
+  int splits;       // jobs that share the keys of a query tile (1: not split)
+  int per_bh;       // items per (batch, head)
+  int items;        // items in all
+  FastDiv f_per_bh, f_heads, f_group, f_sp;
+};
+
+// (batch, head), query tile and key split of an item's two jobs.
+struct CrossItem {
+  int b, h, hk;
+  int qt[2];   // query tile of each job, -1: none
+  int sp[2];   // key split of each job
+  bool shared; // both jobs read the same keys
+};
+
+inline CrossPlan make_cross_plan(int B, int heads, int kv_heads, int n, int m) {
+  CrossPlan p{};
+  p.qtiles = (n + 127) / 128;
+  p.kblocks = (m + 127) / 128;
+  const long long all = (long long)B * heads * p.qtiles;
+  p.tiles = all >= 2 * kCrossPlanSms ? 2 : 1;
+  p.splits = 1;
+  if (all * 2 <= kCrossPlanSms && p.kblocks >= 4) {
+    long long s = 2 * kCrossPlanSms / all;             // two jobs per SM
+    const long long most = p.kblocks / 2;              // at least two blocks per job
+    s = s < most ? s : most;
+    p.splits = int(s < 64 ? s : 64);
+    if (p.splits < 2) p.splits = 1;
+  }
+  if (p.splits > 1)
+    p.per_bh = p.qtiles * ((p.splits + 1) / 2);
+  else
+    p.per_bh = (p.qtiles + p.tiles - 1) / p.tiles;
+  p.items = B * heads * p.per_bh;
+  p.f_per_bh = make_fastdiv(uint32_t(p.per_bh));
+  p.f_heads = make_fastdiv(uint32_t(heads));
+  p.f_group = make_fastdiv(uint32_t(heads / kv_heads));
+  p.f_sp = make_fastdiv(uint32_t((p.splits + 1) / 2));
+  return p;
+}
+
+SQ_HD CrossItem cross_item(const CrossPlan& p, int heads, int i) {
+  CrossItem it;
+  const int bh = fdiv(i, p.f_per_bh), r = i - bh * p.per_bh;
+  it.b = fdiv(bh, p.f_heads);
+  it.h = bh - it.b * heads;
+  it.hk = fdiv(it.h, p.f_group);
+  if (p.splits > 1) {
+    const int qt = fdiv(r, p.f_sp), s = 2 * (r - qt * ((p.splits + 1) / 2));
+    it.qt[0] = qt;
+    it.qt[1] = s + 1 < p.splits ? qt : -1;
+    it.sp[0] = s;
+    it.sp[1] = s + 1;
+    it.shared = false;
+  } else {
+    it.qt[0] = r * p.tiles;
+    it.qt[1] = p.tiles == 2 && it.qt[0] + 1 < p.qtiles ? it.qt[0] + 1 : -1;
+    it.sp[0] = it.sp[1] = 0;
+    it.shared = it.qt[1] >= 0;
+  }
+  return it;
+}
+
+// Key blocks [k0, k0 + nk) of a job and the bound its keys lie below, for `len` keys that may
+// count. nk is at least 1: a job without keys runs one block whose keys are all masked.
+struct CrossRange {
+  int k0, nk, limit;
+};
+SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
+  const int nb = (len + 127) >> 7;
+  const int per = p.splits > 1 ? (nb + p.splits - 1) / p.splits : nb;
+  CrossRange r;
+  r.k0 = sp * per;
+  const int k1 = r.k0 + per < nb ? r.k0 + per : nb;
+  r.nk = k1 - r.k0 > 1 ? k1 - r.k0 : 1;
+  r.limit = k1 * 128 < len ? k1 * 128 : len;
+  return r;
+}
+
+}  // namespace sq
