@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "squad.h"
+#include "cross_bwd_tc.cuh"
 #include "cross_fwd_tc.cuh"
 #include "cross_simt.cuh"
 #include "geometry.h"
@@ -241,6 +242,100 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   return SQUAD_OK;
 }
 
+// ---------------------------------------------------------------- tensor-core backward (bf16)
+
+struct BwdWs {
+  size_t part, total;  // D vector first
+  int splits;
+};
+
+BwdWs bwd_workspace(const squad_cross_desc* d) {
+  BwdWs w{};
+  w.splits = 1;
+  w.part = bwd_rowvec_bytes(d);
+  w.total = w.part;
+  if (d->dtype != SQUAD_BF16) return w;
+  const long long units = (long long)d->B * d->kv_heads * ((d->m + 127) / 128);
+  const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + 127) / 128);
+  w.splits = sq::cross_dkv_splits(units, int(tiles));
+  if (w.splits > 1) w.total += align256(size_t(2) * w.splits * units * 128 * d->d * sizeof(float));
+  return w;
+}
+
+template <int D, bool MASKED>
+squad_status launch_cross_bwd(const sq::HostDevice& dev, const sq::CrossBwdMaps& maps, sq::CrossBwdArgs a,
+                              cudaStream_t st) {
+  squad_status s;
+  static std::atomic<bool> done_q[kMaxDevices], done_kv[kMaxDevices];
+  auto dq = sq::cross_bwd_dq_kernel<D, MASKED>;
+  auto dkv = sq::cross_bwd_dkdv_kernel<D, MASKED>;
+  if ((s = allow_smem(dq, sq::CrossDqLayout<D>::BYTES, dev, done_q)) != SQUAD_OK) return s;
+  if ((s = allow_smem(dkv, sq::CrossDkvLayout<D>::BYTES, dev, done_kv)) != SQUAD_OK) return s;
+  a.items = a.B * a.heads * a.qtiles;
+  dq<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDqLayout<D>::BYTES, st>>>(maps, a);
+  SQ_CUDA(cudaGetLastError());
+  a.items = a.B * a.kv_heads * a.kblocks * a.splits;
+  dkv<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDkvLayout<D>::BYTES, st>>>(maps, a);
+  SQ_CUDA(cudaGetLastError());
+  if (a.splits > 1) {
+    const long long rows = (long long)a.B * a.kv_heads * a.m;
+    const dim3 grid(unsigned((rows * (D / 4) + 255) / 256), 2);
+    sq::cross_join_grads_kernel<D><<<grid, 256, 0, st>>>(a.part, a.splits,
+                                                         (long long)a.B * a.kv_heads * a.kblocks * 128, a.kblocks * 128,
+                                                         a.kv_heads, a.m, rows, a.dk, a.sdk, a.dv, a.sdv);
+    SQ_CUDA(cudaGetLastError());
+  }
+  return SQUAD_OK;
+}
+
+squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c, void* ws,
+                          cudaStream_t st) {
+  sq::CrossBwdMaps maps;
+  sq::CrossBwdArgs a{};
+  a.B = d->B;
+  a.heads = d->heads;
+  a.kv_heads = d->kv_heads;
+  a.group = c.group;
+  a.n = d->n;
+  a.m = d->m;
+  a.qtiles = (d->n + 127) / 128;
+  a.kblocks = (d->m + 127) / 128;
+  const BwdWs w = bwd_workspace(d);
+  a.splits = w.splits;
+  a.f_qtiles = sq::make_fastdiv(uint32_t(a.qtiles));
+  a.f_heads = sq::make_fastdiv(uint32_t(a.heads));
+  a.f_group = sq::make_fastdiv(uint32_t(a.group));
+  a.f_kblocks = sq::make_fastdiv(uint32_t(a.kblocks));
+  a.f_kv_heads = sq::make_fastdiv(uint32_t(a.kv_heads));
+  squad_status s;
+  const int B = d->B, h = d->heads, hk = d->kv_heads, D = d->d;
+  if ((s = encode_rows(&maps.q, dev, c.q, d->q, B, h, d->n, D, &a.q_b, &a.q_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.k, dev, c.k, d->k, B, hk, d->m, D, &a.k_b, &a.k_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.v, dev, c.v, d->v, B, hk, d->m, D, &a.v_b, &a.v_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.dout, dev, c.dout, d->dout, B, h, d->n, D, &a.do_b, &a.do_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.dq, dev, c.dq, d->dq, B, h, d->n, D, &a.dq_b, &a.dq_h)) != SQUAD_OK) return s;
+  a.mask = c.mask;
+  a.scale = c.scale;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  a.o = static_cast<const __nv_bfloat16*>(c.o_in);
+  a.dout = static_cast<const __nv_bfloat16*>(c.dout);
+  a.so = c.so;
+  a.sdo = c.sdo;
+  a.sdk = c.sdk;
+  a.sdv = c.sdv;
+  a.lse = c.lse;
+  a.Drow = c.Drow;
+  a.dk = static_cast<__nv_bfloat16*>(c.dk);
+  a.dv = static_cast<__nv_bfloat16*>(c.dv);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
+  a.err = dev.err;
+  a.timeout_ns = sq::kWaitTimeoutNs;
+  const bool masked = c.mask.lens != nullptr || c.mask.keys != nullptr;
+  if (D == 128)
+    return masked ? launch_cross_bwd<128, true>(dev, maps, a, st) : launch_cross_bwd<128, false>(dev, maps, a, st);
+  return masked ? launch_cross_bwd<64, true>(dev, maps, a, st) : launch_cross_bwd<64, false>(dev, maps, a, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -252,7 +347,7 @@ squad_status squad_cross_workspace_size(const squad_cross_desc* desc, int which,
   if (which == 0)
     *bytes = fwd_workspace(desc).total;
   else if (which == 1)
-    *bytes = bwd_rowvec_bytes(desc);
+    *bytes = bwd_workspace(desc).total;
   else
     return SQUAD_ERR_INVALID_ARG;
   return SQUAD_OK;
@@ -308,7 +403,7 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   a.dv = dv;
   a.Drow = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? simt_cross<__nv_bfloat16, true>(a, st) : simt_cross<float, true>(a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : simt_cross<float, true>(a, st);
 }
 
 // ---------------------------------------------------------------- rotary positions

@@ -1,0 +1,940 @@
+// cross_bwd_tc.cuh - backward of cross attention on the sm_100a tensor cores (bf16).
+//
+// With P = exp(s S - lse), dP = dO V^T, D = rowsum(dO o O), dS = P o (dP - D):
+//   dQ = s dS K,   dK = s dS^T Q,   dV = P^T dO.
+// Two kernels, each with its accumulators in TMEM and nothing added across CTAs by atomics
+// (so the results repeat bitwise): one holds a query tile and walks the keys (dQ), one holds a
+// key tile and walks the queries of its head group (dK, dV). S and dP are computed in both:
+// 7 products of 2 n m d flops in place of the 5 of a single kernel, whose dQ parts (one fp32
+// [n, d] per 128 keys) would have to be added in memory: at m = 512 four times the bytes of dQ
+// in fp32 through L2, more than the two products cost.
+//
+// Rounding: P and dS to bf16 before the products that read them (the tensor core's operand
+// type); D, the statistics and the accumulators in fp32; each gradient once at the end.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "cross_tc.cuh"
+
+namespace sq {
+
+constexpr int kCrossBwdThreads = 512;
+
+struct alignas(64) CrossBwdMaps {
+  CUtensorMap q, k, v, dout, dq;
+};
+
+struct CrossBwdArgs {
+  int B, heads, kv_heads, group, n, m;
+  int qtiles, kblocks;
+  int splits;             // dk, dv kernel: parts of a key tile's queries
+  int items;              // dq kernel: query tiles in all; dk, dv kernel: (key tile, split) units
+  FastDiv f_qtiles, f_heads, f_group, f_kblocks, f_kv_heads;
+  int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h, dq_b, dq_h;  // 1, or 0 where the map has no such extent
+  CrossMask mask;
+  float scale, scale_log2;
+  const __nv_bfloat16 *o, *dout;  // for D
+  CrossStride so, sdo, sdk, sdv;
+  const float* lse;       // [B, heads, n]
+  float* Drow;            // [B, heads, n]: written by the dq kernel, read by the other
+  __nv_bfloat16 *dk, *dv;
+  float* part;            // splits > 1: [dk, dv][split][B, kv_heads, kblocks * 128][D] fp32
+  int* err;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t to) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, to)) != 0;
+}
+
+// ==================================================================== dQ
+//
+// Roles (512 threads):
+//   warps 0-3, 4-7  key columns 0-63 and 64-127 of each block (thread = query row = TMEM lane)
+//   warps 8-11      D of the next tile (from dO and O in memory), then dQ of this one:
+//                   TMEM -> bf16 -> the Q tile in shared memory -> TMA store; their first thread
+//                   then loads the query tile after next into that place
+//   warp 12         key tiles;  warp 15: value tiles and dO;  warp 13: tcgen05.mma
+//   warp 14         zeroes masked rows of key and value tiles
+// TMEM: S of block t at [128 (t & 1), ...), dP at [256, 384), dQ at [384, 384 + D). dS replaces
+// S in place (packed bf16, each half inside its own columns).
+// Per block the tensor core runs S(t+1), dP(t+1), dQ(t); the exponentials of block t+1 run
+// while dP(t+1) and dQ(t) do.
+
+template <int D>
+struct CrossDqLayout {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4, NDO = D == 128 ? 1 : 2;
+  static constexpr int Q_OFF = 0;
+  static constexpr int DO_OFF = 2 * TILE;
+  static constexpr int K_OFF = DO_OFF + NDO * TILE;
+  static constexpr int V_OFF = K_OFF + NK * TILE;
+  static constexpr int D_OFF = V_OFF + NV * TILE;  // D of two tiles
+  static constexpr int BAR_OFF = D_OFF + 2 * 128 * 4;
+  static constexpr int QF = 0, DOF = QF + 2, DOE = DOF + NDO, KF = DOE + NDO, KE = KF + NK, KR = KE + NK, VF = KR + NK,
+                       VE = VF + NV, VR = VE + NV, SF = VR + NV, DPF = SF + 2, DSF = DPF + 1, OF = DSF + 1, OE = OF + 1,
+                       DF = OE + 1, DE = DF + 2, ST = DE + 2, DRAIN = ST + 1, NBAR = DRAIN + 1;
+  static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;
+  static_assert(BYTES <= 232448, "shared memory of one CTA");
+};
+
+template <int D, bool MASKED>
+__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+    cross_bwd_dq_kernel(const __grid_constant__ CrossBwdMaps maps, const __grid_constant__ CrossBwdArgs args) {
+  using Lay = CrossDqLayout<D>;
+  constexpr int DH = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
+  float* d_smem = reinterpret_cast<float*>(smem + Lay::D_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t to = args.timeout_ns;
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(args.err, 0, 1);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Lay::NBAR; ++i) {
+      const int warps = i == Lay::DSF ? 8 : i >= Lay::DE && i < Lay::DE + 2 ? 8 : i == Lay::OE || i == Lay::ST ? 4
+                        : i >= Lay::DF && i < Lay::DF + 2 ? 4 : 1;
+      mbar_init(&bars[i], warps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 12 && lane == 0) {
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.dout);
+    prefetch_tmap(&maps.dq);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t sbase = smem_u32(smem);
+
+  struct Item {
+    int b, h, hk, qt;
+  };
+  auto item_of = [&](int i) -> Item {
+    const int bh = fdiv(i, args.f_qtiles), b = fdiv(bh, args.f_heads), h = bh - b * args.heads;
+    return Item{b, h, fdiv(h, args.f_group), i - bh * args.qtiles};
+  };
+  int len_b = -1, len_v = 0;
+  auto len_of = [&](int b) -> int {
+    if (!MASKED) return args.m;
+    if (b != len_b) {
+      len_v = cross_len(args.mask, b, args.m);
+      len_b = b;
+    }
+    return len_v;
+  };
+  // blocks of a batch row; one (all masked) where no key counts
+  auto blocks_of = [&](int b) -> int {
+    const int nb = (len_of(b) + 127) >> 7;
+    return nb > 1 ? nb : 1;
+  };
+  auto load = [&](uint32_t dst, const CUtensorMap* m, uint64_t* bar, int row, int h, int b) {
+    mbar_arrive_expect_tx(bar, Lay::TILE);
+#pragma unroll
+    for (int c = 0; c < DH; ++c) tma_load_4d(dst + c * kCrossBlk, m, bar, c * 64, row, h, b);
+  };
+  // lets the loads issued into a ring land before the CTA may exit
+  auto drain_ring = [&](int full, uint32_t slots, uint32_t issued) {
+    for (uint32_t s = 0; s < slots; ++s) {
+      const uint32_t uses = issued > s ? (issued - s + slots - 1) / slots : 0;
+      if (uses) mbar_wait_drain(&bars[full + s], (uses - 1) & 1, to);
+    }
+  };
+
+  if (warp == 12) {
+    if (lane == 0) {  // ---------------------------------------------- key tiles
+      uint32_t e = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        const Item it = item_of(i);
+        const int nk = blocks_of(it.b);
+        for (int k = 0; ok && k < nk; ++k) {
+          const uint32_t s = e % Lay::NK;
+          if (!(ok = mbar_wait(&bars[Lay::KE + s], ((e / Lay::NK) & 1) ^ 1, abort_flag, to))) break;
+          load(sbase + Lay::K_OFF + s * Lay::TILE, &maps.k, &bars[Lay::KF + s], k * 128, it.hk * args.k_h, it.b * args.k_b);
+          ++e;
+        }
+      }
+      drain_ring(Lay::KF, Lay::NK, e);
+    }
+  } else if (warp == 15) {
+    if (lane == 0) {  // ---------------------------------------------- value tiles and dO
+      uint32_t e = 0, q = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        const Item it = item_of(i);
+        const int nk = blocks_of(it.b);
+        for (int k = 0; ok && k < nk; ++k) {
+          const uint32_t s = e % Lay::NV;
+          if (!(ok = mbar_wait(&bars[Lay::VE + s], ((e / Lay::NV) & 1) ^ 1, abort_flag, to))) break;
+          load(sbase + Lay::V_OFF + s * Lay::TILE, &maps.v, &bars[Lay::VF + s], k * 128, it.hk * args.v_h, it.b * args.v_b);
+          ++e;
+          if (k == 0) {
+            const uint32_t z = q % Lay::NDO;
+            if (!(ok = mbar_wait(&bars[Lay::DOE + z], ((q / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
+            load(sbase + Lay::DO_OFF + z * Lay::TILE, &maps.dout, &bars[Lay::DOF + z], it.qt * 128, it.h * args.do_h,
+                 it.b * args.do_b);
+            ++q;
+          }
+        }
+      }
+      drain_ring(Lay::VF, Lay::NV, e);
+      drain_ring(Lay::DOF, Lay::NDO, q);
+    }
+  } else if (warp == 14) {
+    if (MASKED) {  // ------------------------------------------------- masked rows to zero
+      uint32_t t = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        const Item it = item_of(i);
+        const int len = len_of(it.b), nk = blocks_of(it.b);
+        for (int k = 0; k < nk; ++k, ++t) {
+          uint32_t w[4];
+          block_words(len - k * 128,
+                      args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + k * 128, lane, w);
+          const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
+          if (!(ok = warp_wait(&bars[Lay::KF + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
+          zero_rows<D>(sbase + Lay::K_OFF + sk * Lay::TILE, w, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::KR + sk]);
+          if (!(ok = warp_wait(&bars[Lay::VF + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
+          zero_rows<D>(sbase + Lay::V_OFF + sv * Lay::TILE, w, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::VR + sv]);
+        }
+      }
+    }
+  } else if (warp == 13) {
+    if (lane == 0) {  // ---------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);  // S, dP: both operands K-major
+      constexpr uint32_t id_q = idesc_bf16_f32(128, D, 0, 1);    // dQ: A (dS) from TMEM, B (K) MN-major
+      constexpr int KREADY = MASKED ? Lay::KR : Lay::KF, VREADY = MASKED ? Lay::VR : Lay::VF;
+      // dQ(t): wait for dS(t), multiply by the key tile, release it
+      auto dq = [&](uint32_t t, uint32_t job, bool first, bool last) -> bool {
+        if (first && job > 0 && !mbar_wait(&bars[Lay::OE], (job - 1) & 1, abort_flag, to)) return false;
+        tc_fence_after();
+        const uint32_t s = t % Lay::NK, ka = sbase + Lay::K_OFF + s * Lay::TILE, a = tmem + 128 * (t & 1);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 384, a + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(ka + kk * 2048, kCrossBlk, 1024), id_q,
+                 (!first || kk > 0) ? 1u : 0u);
+        tc_commit(&bars[Lay::KE + s]);
+        if (last) tc_commit(&bars[Lay::OF]);
+        return true;
+      };
+      uint32_t t = 0, job = 0;
+      bool ok = true, prev = false, prev_first = false, prev_last = false;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
+        const Item it = item_of(i);
+        const int nk = blocks_of(it.b);
+        const uint32_t qa = sbase + Lay::Q_OFF + (job & 1) * Lay::TILE;
+        const uint32_t z = job % Lay::NDO, da = sbase + Lay::DO_OFF + z * Lay::TILE;
+        for (int k = 0; k < nk; ++k, ++t) {
+          const bool first = k == 0, last = k == nk - 1;
+          const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
+          // S(t) into the columns that dQ(t - 2) read dS from (issued before, so behind it)
+          if (!(ok = mbar_wait(&bars[KREADY + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
+          if (first && !(ok = mbar_wait(&bars[Lay::QF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
+          tc_fence_after();
+          const uint32_t ka = sbase + Lay::K_OFF + sk * Lay::TILE, va = sbase + Lay::V_OFF + sv * Lay::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
+            mma_ss(tmem + 128 * (t & 1), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_s,
+                   kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&bars[Lay::SF + (t & 1)]);
+          // dS(t - 1) is written, so dP(t - 1) has been read
+          if (prev && !(ok = mbar_wait(&bars[Lay::DSF], (t - 1) & 1, abort_flag, to))) break;
+          // at a new tile dO has yet to arrive: dQ of the last block goes first
+          if (prev && first && !(ok = dq(t - 1, job - 1, prev_first, prev_last))) break;
+          if (!(ok = mbar_wait(&bars[VREADY + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
+          if (first && !(ok = mbar_wait(&bars[Lay::DOF + z], (job / Lay::NDO) & 1, abort_flag, to))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
+            mma_ss(tmem + 256, sdesc_sw128(da + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&bars[Lay::DPF]);
+          tc_commit(&bars[Lay::VE + sv]);
+          if (last) tc_commit(&bars[Lay::DOE + z]);
+          if (prev && !first && !(ok = dq(t - 1, job, prev_first, prev_last))) break;
+          prev = true;
+          prev_first = first;
+          prev_last = last;
+        }
+      }
+      if (ok && prev && mbar_wait(&bars[Lay::DSF], (t - 1) & 1, abort_flag, to)) dq(t - 1, job - 1, prev_first, prev_last);
+      tc_commit(&bars[Lay::DRAIN]);
+      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ D, dQ
+    const int ew = warp & 3, row = threadIdx.x & 127;
+    constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per load
+    bool ok = true;
+    uint32_t made = 0;  // tiles whose D is made
+    auto make_d = [&](int i) -> bool {
+      const Item it = item_of(i);
+      const uint32_t par = made & 1;
+      if (!warp_wait(&bars[Lay::DE + par], ((made >> 1) & 1) ^ 1, abort_flag, to)) return false;
+      const long long base = ((long long)it.b * args.heads + it.h) * args.n;
+      const int r0 = it.qt * 128 + ew * 32 + lane / LPR, c = (lane % LPR) * 8;
+#pragma unroll 1
+      for (int g = 0; g < 32 / RPI; g += 8) {
+        uint4 xa[8], xb[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int tok = r0 + (g + u) * RPI;
+          xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
+          if (tok < args.n) {
+            xa[u] = __ldg(reinterpret_cast<const uint4*>(args.o + it.b * args.so.b + it.h * args.so.h + tok * args.so.n + c));
+            xb[u] = __ldg(
+                reinterpret_cast<const uint4*>(args.dout + it.b * args.sdo.b + it.h * args.sdo.h + tok * args.sdo.n + c));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t a[4] = {xa[u].x, xa[u].y, xa[u].z, xa[u].w}, b[4] = {xb[u].x, xb[u].y, xb[u].z, xb[u].w};
+          float acc = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), acc);
+            acc = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(b[e] & 0xffff0000u), acc);
+          }
+#pragma unroll
+          for (int z = LPR / 2; z > 0; z >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, z);
+          const int tok = r0 + (g + u) * RPI;
+          if (lane % LPR == 0) {
+            d_smem[par * 128 + tok - it.qt * 128] = acc;
+            if (tok < args.n) args.Drow[base + tok] = acc;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Lay::DF + par]);
+      ++made;
+      return true;
+    };
+    auto load_q = [&](int i, uint32_t job) {
+      const Item it = item_of(i);
+      load(sbase + Lay::Q_OFF + (job & 1) * Lay::TILE, &maps.q, &bars[Lay::QF + (job & 1)], it.qt * 128,
+           it.h * args.q_h, it.b * args.q_b);
+    };
+    uint32_t qloads = 0;
+    if (threadIdx.x == 256) {
+      for (int i = blockIdx.x; qloads < 2 && i < args.items; i += gridDim.x, ++qloads) load_q(i, qloads);
+    }
+    __syncwarp();
+    if (int(blockIdx.x) < args.items) ok = make_d(blockIdx.x);
+    uint32_t job = 0;
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
+      if (i + int(gridDim.x) < args.items && !(ok = make_d(i + gridDim.x))) break;
+      const Item it = item_of(i);
+      if (!(ok = warp_wait(&bars[Lay::OF], job & 1, abort_flag, to))) break;
+      tc_fence_after();
+      const uint32_t t = tmem + (uint32_t(ew * 32) << 16) + 384;
+      const uint32_t tile = sbase + Lay::Q_OFF + (job & 1) * Lay::TILE, stage = tile + row * 128;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(t + c, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[e] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * args.scale,
+                               __uint_as_float(v[8 * j + 2 * e + 1]) * args.scale);
+          const int chunk = ((c & 32) >> 3) + j;
+          st_shared_v4(stage + (c >> 6) * kCrossBlk + ((chunk ^ (row & 7)) << 4), p[0], p[1], p[2], p[3]);
+        }
+      }
+      tc_fence_before();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars[Lay::OE]);
+        mbar_arrive(&bars[Lay::ST]);
+      }
+      if (threadIdx.x == 256) {
+        ok = mbar_wait(&bars[Lay::ST], job & 1, abort_flag, to);
+#pragma unroll
+        for (int c = 0; ok && c < DH; ++c)
+          tma_store_4d(&maps.dq, tile + c * kCrossBlk, c * 64, it.qt * 128, it.h * args.dq_h, it.b * args.dq_b);
+        bulk_commit();
+        bulk_wait_read();
+        const long long next = (long long)i + 2ll * gridDim.x;
+        if (ok && next < args.items) {
+          load_q(int(next), job);
+          ++qloads;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+    }
+    if (threadIdx.x == 256) drain_ring(Lay::QF, 2, qloads);
+  } else {
+    // ------------------------------------------------------------------ P, dS
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const float c2 = args.scale_log2;
+    const uint64_t c2x2 = f2(c2, c2);
+    uint32_t t = 0, job = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
+      const Item it = item_of(i);
+      const int len = len_of(it.b), nk = blocks_of(it.b), tok = it.qt * 128 + row;
+      const bool idle = it.qt * 128 + (warp & 3) * 32 >= args.n;
+      // rows past the last query and rows without keys: P = 2^(s - inf) = 0
+      float lse2 = INFINITY;
+      if (tok < args.n) {
+        const float l = __ldg(args.lse + ((long long)it.b * args.heads + it.h) * args.n + tok);
+        lse2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+      }
+      const uint64_t neg2 = f2(-lse2, -lse2);
+      float Dv = 0.f;
+      for (int k = 0; k < nk; ++k, ++t) {
+        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+        const unsigned char* keys =
+            !MASKED || args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + k * 128;
+        if (len - k * 128 < 128 || keys != nullptr) block_words(len - k * 128, keys, lane, w);
+        const uint32_t wa = g ? w[2] : w[0], wb = g ? w[3] : w[1];
+        const uint32_t tS = tmem + lanes + 128 * (t & 1) + 64 * g, tP = tmem + lanes + 256 + 64 * g;
+        if (!(ok = warp_wait(&bars[Lay::SF + (t & 1)], (t >> 1) & 1, abort_flag, to))) break;
+        tc_fence_after();
+        float p[64];
+        if (!idle) {
+          uint32_t v[2][16];
+          tmem_ld16_async(tS, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&u)[16] = v[c & 1];
+            tmem_ld_wait(u);
+            if (c < 3) tmem_ld16_async(tS + 16 * (c + 1), v[(c + 1) & 1]);
+            const uint32_t word = (c < 2 ? wa : wb) >> (16 * (c & 1)) & 0xffffu;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint64_t z = ffma2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), c2x2, neg2);
+              p[16 * c + e] = ex2_approx(f2_lo(z));
+              p[16 * c + e + 1] = ex2_approx(f2_hi(z));
+            }
+            if (word != 0xffffu) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!((word >> e) & 1u)) p[16 * c + e] = 0.f;
+            }
+          }
+        }
+        if (k == 0) {
+          if (!(ok = warp_wait(&bars[Lay::DF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
+          Dv = d_smem[(job & 1) * 128 + row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::DE + (job & 1)]);
+        }
+        if (!(ok = warp_wait(&bars[Lay::DPF], t & 1, abort_flag, to))) break;
+        tc_fence_after();
+        if (!idle) {
+          const uint64_t nd = f2(-Dv, -Dv);
+          uint32_t v[2][16];
+          tmem_ld16_async(tP, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&u)[16] = v[c & 1];
+            tmem_ld_wait(u);
+            if (c < 3) tmem_ld16_async(tP + 16 * (c + 1), v[(c + 1) & 1]);
+            uint32_t d[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint64_t z = mul2(fadd2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd),
+                                      f2(p[16 * c + e], p[16 * c + e + 1]));
+              d[e >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
+            }
+            tmem_st8(tS + 8 * c, d);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::DSF]);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0 && args.err != nullptr) atomicCAS(args.err, 0, 1);
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ==================================================================== dK, dV
+//
+// A unit is a key tile (128 keys of a key head) and a part of the queries of its head group.
+// Roles (512 threads):
+//   warps 0-3, 4-7  query columns 0-63 and 64-127 of each tile (thread = key row = TMEM lane)
+//   warps 8-11      dK and dV of a finished unit: TMEM -> bf16 rows, or fp32 parts
+//   warp 12         key and value tiles, query tiles;  warp 15: dO;  warp 13: tcgen05.mma
+//   warp 14         -lse log2 e and -D of each query tile into shared memory
+// TMEM: S^T [0,128), dP^T [128,256), dV [256, 256 + D), dK [384, 384 + D). P^T and dS^T replace
+// S^T and dP^T in place (packed bf16, each half inside its own columns).
+// Per query tile the tensor core runs dV(t), S(t+1) once P(t) is there, then dK(t), dP(t+1)
+// once dS(t) is there: four products in turn, with the softmax of one under the products of
+// the other.
+
+template <int D>
+struct CrossDkvLayout {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NQ = D == 128 ? 3 : 4, NDO = D == 128 ? 2 : 4;
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = TILE;
+  static constexpr int Q_OFF = 2 * TILE;
+  static constexpr int DO_OFF = Q_OFF + NQ * TILE;
+  static constexpr int VEC_OFF = DO_OFF + NDO * TILE;  // two tiles of (-lse, -D)
+  static constexpr int BAR_OFF = VEC_OFF + 2 * 256 * 4;
+  static constexpr int KF = 0, KE = 1, VF = 2, VE = 3, QF = 4, QE = QF + NQ, DOF = QE + NQ, DOE = DOF + NDO,
+                       SF = DOE + NDO, PF = SF + 1, DPF = PF + 1, DSF = DPF + 1, ACCF = DSF + 1, ACCE = ACCF + 1,
+                       VECF = ACCE + 1, VECE = VECF + 2, DRAIN = VECE + 2, NBAR = DRAIN + 1;
+  static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;
+  static_assert(BYTES <= 232448, "shared memory of one CTA");
+};
+
+template <int D, bool MASKED>
+__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+    cross_bwd_dkdv_kernel(const __grid_constant__ CrossBwdMaps maps, const __grid_constant__ CrossBwdArgs args) {
+  using Lay = CrossDkvLayout<D>;
+  constexpr int DH = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t to = args.timeout_ns;
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(args.err, 0, 1);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Lay::NBAR; ++i) {
+      const int warps = i == Lay::PF || i == Lay::DSF || (i >= Lay::VECE && i < Lay::VECE + 2) ? 8 : i == Lay::ACCE ? 4 : 1;
+      mbar_init(&bars[i], warps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 12 && lane == 0) {
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.dout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t sbase = smem_u32(smem);
+
+  struct Unit {
+    int b, hk, kb, sp;
+    int t0, t1;   // query tiles of the head group (head-major) in this unit
+    int limit;    // keys of the tile below it may count
+  };
+  int len_b = -1, len_v = 0;
+  // splits are the slowest index: the key tiles that share query tiles run side by side
+  auto unit_of = [&](int i) -> Unit {
+    Unit u;
+    const int per = args.B * args.kv_heads * args.kblocks;
+    u.sp = i / per;
+    const int j = i - u.sp * per;
+    const int bh = fdiv(j, args.f_kblocks);
+    u.kb = j - bh * args.kblocks;
+    u.b = fdiv(bh, args.f_kv_heads);
+    u.hk = bh - u.b * args.kv_heads;
+    if (MASKED && u.b != len_b) {
+      len_v = cross_len(args.mask, u.b, args.m);
+      len_b = u.b;
+    }
+    u.limit = (MASKED ? len_v : args.m) - u.kb * 128;
+    const int tiles = args.group * args.qtiles, part = (tiles + args.splits - 1) / args.splits;
+    u.t0 = u.sp * part;
+    u.t1 = u.t0 + part < tiles ? u.t0 + part : tiles;
+    if (u.t0 > tiles) u.t0 = tiles;
+    if (u.limit <= 0) u.t1 = u.t0;  // no key of the tile counts: nothing to add up
+    return u;
+  };
+  auto load = [&](uint32_t dst, const CUtensorMap* m, uint64_t* bar, int row, int h, int b) {
+    mbar_arrive_expect_tx(bar, Lay::TILE);
+#pragma unroll
+    for (int c = 0; c < DH; ++c) tma_load_4d(dst + c * kCrossBlk, m, bar, c * 64, row, h, b);
+  };
+  auto drain_ring = [&](int full, uint32_t slots, uint32_t issued) {
+    for (uint32_t s = 0; s < slots; ++s) {
+      const uint32_t uses = issued > s ? (issued - s + slots - 1) / slots : 0;
+      if (uses) mbar_wait_drain(&bars[full + s], (uses - 1) & 1, to);
+    }
+  };
+
+  if (warp == 12) {
+    if (lane == 0) {  // ---------------------------------------------- key, value and query tiles
+      uint32_t e = 0, units = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        const Unit u = unit_of(i);
+        if (u.t0 >= u.t1) continue;
+        for (int t = u.t0; ok && t < u.t1; ++t) {
+          if (t == u.t0) {
+            if (!(ok = mbar_wait(&bars[Lay::KE], (units & 1) ^ 1, abort_flag, to))) break;
+            load(sbase + Lay::K_OFF, &maps.k, &bars[Lay::KF], u.kb * 128, u.hk * args.k_h, u.b * args.k_b);
+          }
+          const int g = fdiv(t, args.f_qtiles), h = u.hk * args.group + g;
+          const uint32_t s = e % Lay::NQ;
+          if (!(ok = mbar_wait(&bars[Lay::QE + s], ((e / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
+          load(sbase + Lay::Q_OFF + s * Lay::TILE, &maps.q, &bars[Lay::QF + s], (t - g * args.qtiles) * 128,
+               h * args.q_h, u.b * args.q_b);
+          ++e;
+        }
+        ++units;
+      }
+      drain_ring(Lay::KF, 1, units);
+      drain_ring(Lay::QF, Lay::NQ, e);
+    }
+  } else if (warp == 15) {
+    if (lane == 0) {  // ---------------------------------------------- value and dO tiles
+      uint32_t e = 0, units = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        const Unit u = unit_of(i);
+        if (u.t0 >= u.t1) continue;
+        for (int t = u.t0; ok && t < u.t1; ++t) {
+          if (t == u.t0) {
+            if (!(ok = mbar_wait(&bars[Lay::VE], (units & 1) ^ 1, abort_flag, to))) break;
+            load(sbase + Lay::V_OFF, &maps.v, &bars[Lay::VF], u.kb * 128, u.hk * args.v_h, u.b * args.v_b);
+          }
+          const int g = fdiv(t, args.f_qtiles), h = u.hk * args.group + g;
+          const uint32_t s = e % Lay::NDO;
+          if (!(ok = mbar_wait(&bars[Lay::DOE + s], ((e / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
+          load(sbase + Lay::DO_OFF + s * Lay::TILE, &maps.dout, &bars[Lay::DOF + s], (t - g * args.qtiles) * 128,
+               h * args.do_h, u.b * args.do_b);
+          ++e;
+        }
+        ++units;
+      }
+      drain_ring(Lay::VF, 1, units);
+      drain_ring(Lay::DOF, Lay::NDO, e);
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------------------------ statistics of the query tiles
+    uint32_t t_all = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+      const Unit u = unit_of(i);
+      for (int t = u.t0; t < u.t1; ++t, ++t_all) {
+        const int g = fdiv(t, args.f_qtiles), h = u.hk * args.group + g, tok = (t - g * args.qtiles) * 128 + lane * 4;
+        const long long base = ((long long)u.b * args.heads + h) * args.n + tok;
+        float l[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // queries past the last and queries without keys: P = 2^(s - inf) = 0
+          l[e] = -INFINITY;
+          d[e] = 0.f;
+          if (tok + e < args.n) {
+            const float x = __ldg(args.lse + base + e);
+            l[e] = x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
+            d[e] = -__ldg(args.Drow + base + e);
+          }
+        }
+        const uint32_t s = t_all & 1;
+        if (!(ok = warp_wait(&bars[Lay::VECE + s], ((t_all >> 1) & 1) ^ 1, abort_flag, to))) break;
+        float* vec = reinterpret_cast<float*>(smem + Lay::VEC_OFF) + s * 256;
+        *reinterpret_cast<float4*>(vec + lane * 4) = make_float4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<float4*>(vec + 128 + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::VECF + s]);
+      }
+    }
+  } else if (warp == 13) {
+    if (lane == 0) {  // ---------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t id_acc = idesc_bf16_f32(128, D, 0, 1);
+      const uint32_t ka = sbase + Lay::K_OFF, va = sbase + Lay::V_OFF;
+      bool ok = true;
+      // the (unit, tile) pairs in order, with one pair of look-ahead
+      struct Step {
+        int i, t, t0, t1;
+        uint32_t unit;
+        bool ok;
+      };
+      auto seek = [&](int i, uint32_t unit) -> Step {
+        for (; i < args.items; i += gridDim.x) {
+          const Unit u = unit_of(i);
+          if (u.t0 < u.t1) return Step{i, u.t0, u.t0, u.t1, unit, true};
+        }
+        return Step{i, 0, 0, 0, unit, false};
+      };
+      auto after = [&](const Step& s) -> Step {
+        if (s.t + 1 < s.t1) return Step{s.i, s.t + 1, s.t0, s.t1, s.unit, true};
+        return seek(s.i + gridDim.x, s.unit + 1);
+      };
+      auto s_mma = [&](const Step& s, uint32_t e) -> bool {
+        const uint32_t z = e % Lay::NQ, qa = sbase + Lay::Q_OFF + z * Lay::TILE;
+        if (s.t == s.t0 && !mbar_wait(&bars[Lay::KF], s.unit & 1, abort_flag, to)) return false;
+        if (!mbar_wait(&bars[Lay::QF + z], (e / Lay::NQ) & 1, abort_flag, to)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
+          mma_ss(tmem, sdesc_sw128(ka + off, 16, 1024), sdesc_sw128(qa + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars[Lay::SF]);
+        if (s.t == s.t1 - 1) tc_commit(&bars[Lay::KE]);
+        return true;
+      };
+      auto dp_mma = [&](const Step& s, uint32_t e) -> bool {
+        const uint32_t z = e % Lay::NDO, da = sbase + Lay::DO_OFF + z * Lay::TILE;
+        if (s.t == s.t0 && !mbar_wait(&bars[Lay::VF], s.unit & 1, abort_flag, to)) return false;
+        if (!mbar_wait(&bars[Lay::DOF + z], (e / Lay::NDO) & 1, abort_flag, to)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
+          mma_ss(tmem + 128, sdesc_sw128(va + off, 16, 1024), sdesc_sw128(da + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars[Lay::DPF]);
+        if (s.t == s.t1 - 1) tc_commit(&bars[Lay::VE]);
+        return true;
+      };
+      uint32_t e = 0;
+      Step cur = seek(blockIdx.x, 0);
+      if (cur.ok) ok = s_mma(cur, 0) && dp_mma(cur, 0);
+      while (ok && cur.ok) {
+        const Step nxt = after(cur);
+        const bool first = cur.t == cur.t0, last = cur.t == cur.t1 - 1;
+        // dV += P^T dO (the unit's first overwrites what the epilogue has drained)
+        if (!(ok = mbar_wait(&bars[Lay::PF], e & 1, abort_flag, to))) break;
+        if (first && cur.unit > 0 && !(ok = mbar_wait(&bars[Lay::ACCE], (cur.unit - 1) & 1, abort_flag, to))) break;
+        tc_fence_after();
+        const uint32_t zo = e % Lay::NDO, da = sbase + Lay::DO_OFF + zo * Lay::TILE;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(da + kk * 2048, kCrossBlk, 1024), id_acc,
+                 (!first || kk > 0) ? 1u : 0u);
+        tc_commit(&bars[Lay::DOE + zo]);
+        if (nxt.ok && !(ok = s_mma(nxt, e + 1))) break;
+        // dK += dS^T Q
+        if (!(ok = mbar_wait(&bars[Lay::DSF], e & 1, abort_flag, to))) break;
+        tc_fence_after();
+        const uint32_t zq = e % Lay::NQ, qa = sbase + Lay::Q_OFF + zq * Lay::TILE;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(qa + kk * 2048, kCrossBlk, 1024),
+                 id_acc, (!first || kk > 0) ? 1u : 0u);
+        tc_commit(&bars[Lay::QE + zq]);
+        if (last) tc_commit(&bars[Lay::ACCF]);
+        if (nxt.ok && !(ok = dp_mma(nxt, e + 1))) break;
+        cur = nxt;
+        ++e;
+      }
+      tc_commit(&bars[Lay::DRAIN]);
+      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ dK, dV
+    const int ew = warp & 3, row = threadIdx.x & 127;
+    const size_t rows_all = size_t(args.B) * args.kv_heads * args.kblocks * 128;
+    uint32_t units = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+      const Unit u = unit_of(i);
+      const int key = u.kb * 128 + row;
+      bool live = row < u.limit;
+      if (MASKED && live && args.mask.keys != nullptr) live = __ldg(args.mask.keys + u.b * args.mask.stride + key) != 0;
+      const bool any = u.t0 < u.t1;
+      if (!any) live = false;
+      if (any) {
+        if (!(ok = warp_wait(&bars[Lay::ACCF], units & 1, abort_flag, to))) break;
+        tc_fence_after();
+      }
+      const uint32_t t = tmem + (uint32_t(ew * 32) << 16);
+      const size_t prow = size_t(u.sp) * rows_all + (size_t(u.b) * args.kv_heads + u.hk) * args.kblocks * 128 + key;
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {  // 0: dK, 1: dV
+        const uint32_t acc = t + (which ? 256 : 384);
+        const float sc = which ? 1.f : args.scale;
+        const CrossStride& st = which ? args.sdv : args.sdk;
+        __nv_bfloat16* out = (which ? args.dv : args.dk) + u.b * st.b + u.hk * st.h + (long long)key * st.n;
+        float* part = args.part + (which * size_t(args.splits) * rows_all + prow) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          if (any) {
+            tmem_ld32(acc + c, v);
+          }
+          // keys that do not count get zeros, whatever the accumulator holds
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = live ? __float_as_uint(__uint_as_float(v[e]) * sc) : 0u;
+          if (args.splits > 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          } else if (key < args.m) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(out + c + e) =
+                  make_uint4(pack_bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                             pack_bf16x2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                             pack_bf16x2(__uint_as_float(v[e + 4]), __uint_as_float(v[e + 5])),
+                             pack_bf16x2(__uint_as_float(v[e + 6]), __uint_as_float(v[e + 7])));
+          }
+        }
+      }
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::ACCE]);
+        ++units;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ P^T, dS^T
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + 64 * g, tP = tmem + lanes + 128 + 64 * g;
+    const float c2 = args.scale_log2;
+    const uint64_t c2x2 = f2(c2, c2);
+    uint32_t e = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+      const Unit u = unit_of(i);
+      // a warp whose key rows all lie past the last has nothing to compute; rows that do not
+      // count are left to the epilogue, which writes zeros for them
+      const bool idle = (warp & 3) * 32 >= u.limit;
+      for (int t = u.t0; t < u.t1; ++t, ++e) {
+        const uint32_t s = e & 1;
+        const uint32_t vec = sbase + Lay::VEC_OFF + s * 1024 + g * 256;
+        if (!(ok = warp_wait(&bars[Lay::VECF + s], (e >> 1) & 1, abort_flag, to))) break;
+        if (!(ok = warp_wait(&bars[Lay::SF], e & 1, abort_flag, to))) break;
+        tc_fence_after();
+        float p[64];
+        if (!idle) {
+          uint32_t v[2][16];
+          tmem_ld16_async(tS, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[16] = v[c & 1];
+            tmem_ld_wait(x);
+            if (c < 3) tmem_ld16_async(tS + 16 * (c + 1), v[(c + 1) & 1]);
+            uint32_t pk[8];
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+              const uint4 l = ld_shared_v4(vec + (16 * c + q) * 4);
+              const uint64_t z0 = ffma2(f2(__uint_as_float(x[q]), __uint_as_float(x[q + 1])), c2x2,
+                                        f2(__uint_as_float(l.x), __uint_as_float(l.y)));
+              const uint64_t z1 = ffma2(f2(__uint_as_float(x[q + 2]), __uint_as_float(x[q + 3])), c2x2,
+                                        f2(__uint_as_float(l.z), __uint_as_float(l.w)));
+              float* o = p + 16 * c + q;
+              o[0] = ex2_approx(f2_lo(z0));
+              o[1] = ex2_approx(f2_hi(z0));
+              o[2] = ex2_approx(f2_lo(z1));
+              o[3] = ex2_approx(f2_hi(z1));
+              pk[q >> 1] = pack_bf16x2(o[0], o[1]);
+              pk[(q >> 1) + 1] = pack_bf16x2(o[2], o[3]);
+            }
+            tmem_st8(tS + 8 * c, pk);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::PF]);
+        if (!(ok = warp_wait(&bars[Lay::DPF], e & 1, abort_flag, to))) break;
+        tc_fence_after();
+        if (!idle) {
+          uint32_t v[2][16];
+          tmem_ld16_async(tP, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[16] = v[c & 1];
+            tmem_ld_wait(x);
+            if (c < 3) tmem_ld16_async(tP + 16 * (c + 1), v[(c + 1) & 1]);
+            uint32_t d[8];
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+              const uint4 l = ld_shared_v4(vec + 512 + (16 * c + q) * 4);
+              const float* o = p + 16 * c + q;
+              const uint64_t z0 = mul2(fadd2(f2(__uint_as_float(x[q]), __uint_as_float(x[q + 1])),
+                                             f2(__uint_as_float(l.x), __uint_as_float(l.y))),
+                                       f2(o[0], o[1]));
+              const uint64_t z1 = mul2(fadd2(f2(__uint_as_float(x[q + 2]), __uint_as_float(x[q + 3])),
+                                             f2(__uint_as_float(l.z), __uint_as_float(l.w))),
+                                       f2(o[2], o[3]));
+              d[q >> 1] = pack_bf16x2(f2_lo(z0), f2_hi(z0));
+              d[(q >> 1) + 1] = pack_bf16x2(f2_lo(z1), f2_hi(z1));
+            }
+            tmem_st8(tP + 8 * c, d);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[Lay::DSF]);
+          mbar_arrive(&bars[Lay::VECE + s]);
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0 && args.err != nullptr) atomicCAS(args.err, 0, 1);
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dk, dv = sum of their parts in order of the splits, 4 channels per thread.
+template <int D>
+__global__ void __launch_bounds__(256) cross_join_grads_kernel(const float* __restrict__ part, int splits,
+                                                               long long part_rows, int mpad, int kv_heads, int m,
+                                                               long long rows, __nv_bfloat16* dk, CrossStride sdk,
+                                                               __nv_bfloat16* dv, CrossStride sdv) {
+  constexpr int C = D / 4;
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long r = id / C;  // (b, kv head, key) of the unpadded rows
+  if (r >= rows) return;
+  const int c = int(id - r * C) * 4, which = blockIdx.y;
+  const long long bh = r / m;
+  const int j = int(r - bh * m), b = int(bh / kv_heads), h = int(bh - (long long)b * kv_heads);
+  const float* p = part + ((which * (long long)splits) * part_rows + bh * mpad + j) * D + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < splits; ++s) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p + s * part_rows * D));
+    a.x += x.x;
+    a.y += x.y;
+    a.z += x.z;
+    a.w += x.w;
+  }
+  const CrossStride& st = which ? sdv : sdk;
+  *reinterpret_cast<uint2*>((which ? dv : dk) + b * st.b + h * st.h + j * st.n + c) =
+      make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+}
+
+}  // namespace sq

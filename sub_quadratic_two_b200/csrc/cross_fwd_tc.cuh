@@ -27,13 +27,11 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 #include "cross_plan.h"
-#include "cross_simt.cuh"
-#include "sm100.cuh"
+#include "cross_tc.cuh"
 
 namespace sq {
 
 constexpr int kCrossThreads = 512;
-constexpr uint32_t kCrossBlk = 128 * 128;  // bytes of a 64-column block of a 128-row bf16 tile
 
 struct alignas(64) CrossMaps {
   CUtensorMap q, k, v, o;
@@ -66,60 +64,6 @@ struct CrossFwdLayout {
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-
-// TMEM loads without their wait, so that several are in flight: pair with tmem_ld_wait.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// Orders the registers of a preceding asynchronous load behind its completion.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
-// Which of the 128 keys of a block count, as four words (the same in every lane). limit: keys
-// of the block below it may count (any sign); keys: the mask bytes of the block, or nullptr.
-__device__ __forceinline__ void block_words(int limit, const unsigned char* keys, int lane, uint32_t (&w)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int l = limit - 32 * j;
-    w[j] = l >= 32 ? ~0u : l <= 0 ? 0u : (1u << l) - 1u;
-    if (keys != nullptr) w[j] &= __ballot_sync(0xffffffffu, lane < l && __ldg(keys + 32 * j + lane) != 0);
-  }
-}
 
 // The order of a CTA's key and value tiles: the walk that the loader, the masker and the MMA
 // issuer share. on_pv(x, e, first, last, free): P V of job x's pending block, values at ring
@@ -303,18 +247,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           uint32_t w[4];
           block_words(limit - kb * 128,
                       args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + kb * 128, lane, w);
-          if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((w[j] >> lane) & 1u) continue;
-              const uint32_t row = sbase + Lay::KV_OFF + s * Lay::TILE + (32 * j + lane) * 128;
-#pragma unroll
-              for (int c = 0; c < DH; ++c)
-#pragma unroll
-                for (int z = 0; z < 8; ++z) st_shared_v4(row + c * kCrossBlk + ((z ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
-          }
+          zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);

@@ -96,4 +96,22 @@ SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   return r;
 }
 
+// How many parts the queries of a key tile are cut into (dk, dv kernel): `units` key tiles of
+// `tiles` query tiles each over the SMs, in the time of one query tile (about 1.1 us at d = 128):
+// rounds of units * s over the SMs, each ceil(tiles / s) tiles and 1.5 to fill and drain, plus,
+// for s > 1, the join kernel (2) and its traffic (0.05 for each part of 128 keys).
+inline int cross_dkv_splits(long long units, int tiles) {
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= tiles && s <= 64; ++s) {
+    const double rounds = double((units * s + kCrossPlanSms - 1) / kCrossPlanSms);
+    const double cost = rounds * (double((tiles + s - 1) / s) + 1.5) + (s > 1 ? 2.0 + 0.05 * double(units) * s : 0.0);
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 }  // namespace sq
