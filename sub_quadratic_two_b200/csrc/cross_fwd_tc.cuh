@@ -32,6 +32,9 @@
 namespace sq {
 
 constexpr int kCrossThreads = 512;
+// Registers per thread: the eight softmax warps hold a whole row of scores (128), the others
+// need few. 256 * 184 + 256 * 72 = 512 * 128, the block's share at launch.
+constexpr int kCrossSoftmaxRegs = 184, kCrossOtherRegs = 72;
 
 struct alignas(64) CrossMaps {
   CUtensorMap q, k, v, o;
@@ -185,150 +188,154 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     return flush(0) && flush(1);
   };
 
-  if (warp == 12) {
-    // ================================================================ key and value loads
-    if (lane == 0) {
-      uint32_t issued = 0;
-      auto load = [&](uint32_t e, const CUtensorMap* m, int h, int b, int kb) -> bool {
-        const uint32_t s = e % Lay::NKV;
-        if (!mbar_wait(&bars[Lay::KVE + s], ((e / Lay::NKV) & 1) ^ 1, abort_flag, to)) return false;
-        mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
-#pragma unroll
-        for (int c = 0; c < DH; ++c)
-          tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, kb * 128, h, b);
-        issued = e + 1;
-        return true;
-      };
-      walk(
-          [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int) -> bool {
-            return !fresh || load(e, &maps.v, it.hk * args.v_h, it.b * args.v_b, kb);
-          },
-          [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int) -> bool {
-            return !fresh || load(e, &maps.k, it.hk * args.k_h, it.b * args.k_b, kb);
-          });
-      // let every issued load land before the CTA may exit
-      for (uint32_t s = 0; s < uint32_t(Lay::NKV); ++s) {
-        const uint32_t uses = issued > s ? (issued - s + Lay::NKV - 1) / Lay::NKV : 0;
-        if (uses) mbar_wait_drain(&bars[Lay::KVF + s], (uses - 1) & 1, to);
-      }
-    }
-  } else if (warp == 15) {
-    // ================================================================ query loads
-    if (lane == 0) {
-      uint32_t q = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
-        const CrossItem it = cross_item(plan, args.heads, i);
-        for (int x = 0; ok && x < 2; ++x) {
-          if (it.qt[x] < 0) continue;
-          const uint32_t s = q % Lay::NQ;
-          if (!(ok = mbar_wait(&bars[Lay::QE + s], ((q / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
-          mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
+  if (warp >= 12) {
+    regs_give<kCrossOtherRegs>();
+    if (warp == 12) {
+      // ================================================================ key and value loads
+      if (lane == 0) {
+        uint32_t issued = 0;
+        auto load = [&](uint32_t e, const CUtensorMap* m, int h, int b, int kb) -> bool {
+          const uint32_t s = e % Lay::NKV;
+          if (!mbar_wait_inline(&bars[Lay::KVE + s], ((e / Lay::NKV) & 1) ^ 1, abort_flag, to)) return false;
+          mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + s], c * 64,
-                        it.qt[x] * 128, it.h * args.q_h, it.b * args.q_b);
-          ++q;
+            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, kb * 128, h, b);
+          issued = e + 1;
+          return true;
+        };
+        walk(
+            [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int) -> bool {
+              return !fresh || load(e, &maps.v, it.hk * args.v_h, it.b * args.v_b, kb);
+            },
+            [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int) -> bool {
+              return !fresh || load(e, &maps.k, it.hk * args.k_h, it.b * args.k_b, kb);
+            });
+        // let every issued load land before the CTA may exit
+        for (uint32_t s = 0; s < uint32_t(Lay::NKV); ++s) {
+          const uint32_t uses = issued > s ? (issued - s + Lay::NKV - 1) / Lay::NKV : 0;
+          if (uses) mbar_wait_drain(&bars[Lay::KVF + s], (uses - 1) & 1, to);
         }
       }
-      for (uint32_t s = 0; s < uint32_t(Lay::NQ); ++s) {
-        const uint32_t uses = q > s ? (q - s + Lay::NQ - 1) / Lay::NQ : 0;
-        if (uses) mbar_wait_drain(&bars[Lay::QF + s], (uses - 1) & 1, to);
-      }
-    }
-  } else if (warp == 14) {
-    // ================================================================ masked rows to zero
-    if (MASKED) {
-      auto fix = [&](uint32_t e, const CrossItem& it, int kb, int limit, bool zero) -> bool {
-        const uint32_t s = e % Lay::NKV;
-        const bool ok = mbar_wait(&bars[Lay::KVF + s], (e / Lay::NKV) & 1, abort_flag, to);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        if (zero) {
-          uint32_t w[4];
-          block_words(limit - kb * 128,
-                      args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + kb * 128, lane, w);
-          zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
-          __syncwarp();
+    } else if (warp == 15) {
+      // ================================================================ query loads
+      if (lane == 0) {
+        uint32_t q = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+          for (int x = 0; ok && x < 2; ++x) {
+            if (it.qt[x] < 0) continue;
+            const uint32_t s = q % Lay::NQ;
+            if (!(ok = mbar_wait_inline(&bars[Lay::QE + s], ((q / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
+            mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
+#pragma unroll
+            for (int c = 0; c < DH; ++c)
+              tma_load_4d(sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + s], c * 64,
+                          it.qt[x] * 128, it.h * args.q_h, it.b * args.q_b);
+            ++q;
+          }
         }
-        if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);
-        return true;
-      };
-      walk(
-          [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
-            return !fresh || fix(e, it, kb, limit, true);
-          },
-          [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
-            return !fresh || fix(e, it, kb, limit, false);  // masked scores are replaced, not multiplied
-          });
-    }
-  } else if (warp == 13) {
-    // ================================================================ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
-      constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
-      uint32_t qn = 0;                    // query tiles taken
-      uint32_t blocks[2] = {0, 0};        // P V products issued per job slot
-      uint32_t jobs[2] = {0, 0};          // jobs begun per job slot
-      uint32_t qslot[2] = {0, 0};
-      walk(
-          [&](int x, uint32_t e, bool, bool done, bool first, bool last, const CrossItem&, int, int) -> bool {
-            const uint32_t s = e % Lay::NKV, par = blocks[x] & 1;
-            if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-            // the job's first product overwrites O: the epilogue has drained the last job's
-            if (first) {
-              if (jobs[x] > 0 && !mbar_wait(&bars[Lay::OE + x], (jobs[x] - 1) & 1, abort_flag, to)) return false;
-              ++jobs[x];
-            }
-            if (!mbar_wait(&bars[Lay::PF + x], par, abort_flag, to)) return false;
-            tc_fence_after();
-            const uint32_t va = sbase + Lay::KV_OFF + s * Lay::TILE;
-            const uint32_t o = tmem + 256 + D * x, p = tmem + 128 * x;
+        for (uint32_t s = 0; s < uint32_t(Lay::NQ); ++s) {
+          const uint32_t uses = q > s ? (q - s + Lay::NQ - 1) / Lay::NQ : 0;
+          if (uses) mbar_wait_drain(&bars[Lay::QF + s], (uses - 1) & 1, to);
+        }
+      }
+    } else if (warp == 14) {
+      // ================================================================ masked rows to zero
+      if (MASKED) {
+        auto fix = [&](uint32_t e, const CrossItem& it, int kb, int limit, bool zero) -> bool {
+          const uint32_t s = e % Lay::NKV;
+          const bool ok = mbar_wait_inline(&bars[Lay::KVF + s], (e / Lay::NKV) & 1, abort_flag, to);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          if (zero) {
+            uint32_t w[4];
+            block_words(limit - kb * 128,
+                        args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + kb * 128, lane, w);
+            zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);
+          return true;
+        };
+        walk(
+            [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
+              return !fresh || fix(e, it, kb, limit, true);
+            },
+            [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
+              return !fresh || fix(e, it, kb, limit, false);  // masked scores are replaced, not multiplied
+            });
+      }
+    } else if (warp == 13) {
+      // ================================================================ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
+        constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
+        uint32_t qn = 0;                    // query tiles taken
+        uint32_t blocks[2] = {0, 0};        // P V products issued per job slot
+        uint32_t jobs[2] = {0, 0};          // jobs begun per job slot
+        uint32_t qslot[2] = {0, 0};
+        walk(
+            [&](int x, uint32_t e, bool, bool done, bool first, bool last, const CrossItem&, int, int) -> bool {
+              const uint32_t s = e % Lay::NKV, par = blocks[x] & 1;
+              if (!mbar_wait_inline(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
+              // the job's first product overwrites O: the epilogue has drained the last job's
+              if (first) {
+                if (jobs[x] > 0 && !mbar_wait_inline(&bars[Lay::OE + x], (jobs[x] - 1) & 1, abort_flag, to)) return false;
+                ++jobs[x];
+              }
+              if (!mbar_wait_inline(&bars[Lay::PF + x], par, abort_flag, to)) return false;
+              tc_fence_after();
+              const uint32_t va = sbase + Lay::KV_OFF + s * Lay::TILE;
+              const uint32_t o = tmem + 256 + D * x, p = tmem + 128 * x;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, (!first || kk > 0) ? 1u : 0u);
-            if (!mbar_wait(&bars[Lay::PF2 + x], par, abort_flag, to)) return false;
-            tc_fence_after();
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, (!first || kk > 0) ? 1u : 0u);
+              if (!mbar_wait_inline(&bars[Lay::PF2 + x], par, abort_flag, to)) return false;
+              tc_fence_after();
 #pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, 1u);
-            if (done) tc_commit(&bars[Lay::KVE + s]);
-            if (last) tc_commit(&bars[Lay::OF + x]);
-            ++blocks[x];
-            return true;
-          },
-          [&](int x, uint32_t e, bool, bool done, bool first, const CrossItem&, int, int) -> bool {
-            const uint32_t s = e % Lay::NKV;
-            if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-            if (first) {
-              qslot[x] = qn % Lay::NQ;
-              if (!mbar_wait(&bars[Lay::QF + qslot[x]], (qn / Lay::NQ) & 1, abort_flag, to)) return false;
-              ++qn;
-            }
-            tc_fence_after();
-            // S overwrites the columns that this job's previous P V reads P from: the tensor
-            // core runs the products of one thread in issue order
-            const uint32_t qa = sbase + Lay::Q_OFF + qslot[x] * Lay::TILE, ka = sbase + Lay::KV_OFF + s * Lay::TILE;
+              for (int kk = 4; kk < 8; ++kk)
+                mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, 1u);
+              if (done) tc_commit(&bars[Lay::KVE + s]);
+              if (last) tc_commit(&bars[Lay::OF + x]);
+              ++blocks[x];
+              return true;
+            },
+            [&](int x, uint32_t e, bool, bool done, bool first, const CrossItem&, int, int) -> bool {
+              const uint32_t s = e % Lay::NKV;
+              if (!mbar_wait_inline(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
+              if (first) {
+                qslot[x] = qn % Lay::NQ;
+                if (!mbar_wait_inline(&bars[Lay::QF + qslot[x]], (qn / Lay::NQ) & 1, abort_flag, to)) return false;
+                ++qn;
+              }
+              tc_fence_after();
+              // S overwrites the columns that this job's previous P V reads P from: the tensor
+              // core runs the products of one thread in issue order
+              const uint32_t qa = sbase + Lay::Q_OFF + qslot[x] * Lay::TILE, ka = sbase + Lay::KV_OFF + s * Lay::TILE;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-              mma_ss(tmem + 128 * x, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_s,
-                     kk > 0 ? 1u : 0u);
-            }
-            tc_commit(&bars[Lay::SF + x]);
-            if (done) tc_commit(&bars[Lay::KVE + s]);
-            return true;
-          });
-      tc_commit(&bars[Lay::DRAIN]);
-      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
+                mma_ss(tmem + 128 * x, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_s,
+                       kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&bars[Lay::SF + x]);
+              if (done) tc_commit(&bars[Lay::KVE + s]);
+              return true;
+            });
+        tc_commit(&bars[Lay::DRAIN]);
+        mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+      }
     }
   } else if (warp >= 8) {
     // ================================================================ epilogue
+    regs_give<kCrossOtherRegs>();
     const int row = threadIdx.x & 127;
     uint32_t q = 0, jobs[2] = {0, 0};
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
     };
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           mbar_arrive(&bars[Lay::ST]);
         }
         if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = mbar_wait(&bars[Lay::ST], (q - 1) & 1, abort_flag, to);
+          ok = mbar_wait_inline(&bars[Lay::ST], (q - 1) & 1, abort_flag, to);
 #pragma unroll
           for (int c = 0; ok && c < DH; ++c)
             tma_store_4d(&maps.o, sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, c * 64, it.qt[x] * 128,
@@ -408,6 +415,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     }
   } else {
     // ================================================================ softmax
+    regs_take<kCrossSoftmaxRegs>();
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + 128 * x;
     const uint32_t tO = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     uint32_t sc = 0, jobs = 0;
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
     };
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
@@ -444,32 +452,27 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           continue;
         }
-        // ---- row maximum; masked scores become -inf, chunks of 32 without a key are skipped
+        // ---- row maximum; masked scores become -inf
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
         float mx = -INFINITY;
-        auto chunk_max = [&](uint32_t (&v)[32], uint32_t word) {
-          if (word != ~0u) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(v[c]);
+          if (w[c] != ~0u) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!((word >> e) & 1u)) v[e] = 0xff800000u;
+              if (!((w[c] >> e) & 1u)) v[c][e] = 0xff800000u;
           }
           float a[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[j] = fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 4]));
+          for (int j = 0; j < 4; ++j) a[j] = fmaxf(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 4]));
 #pragma unroll
           for (int e = 8; e < 32; e += 8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] = fmax3(a[j], __uint_as_float(v[e + j]), __uint_as_float(v[e + j + 4]));
+            for (int j = 0; j < 4; ++j) a[j] = fmax3(a[j], __uint_as_float(v[c][e + j]), __uint_as_float(v[c][e + j + 4]));
           mx = fmax3(mx, fmax3(a[0], a[1], a[2]), a[3]);
-        };
-        {
-          uint32_t v[2][32];
-          tmem_ld32_async(tS, v[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait(v[c & 1]);
-            if (c < 3) tmem_ld32_async(tS + 32 * (c + 1), v[(c + 1) & 1]);
-            chunk_max(v[c & 1], w[c]);
-          }
         }
         // the first block sets the maximum; a later one moves it only when it grows by more
         // than 2^8 (then O and the sum are rescaled), else its probabilities may exceed 1
@@ -494,40 +497,26 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         const float neg = m_use == -INFINITY ? 0.f : -m_use * c2;  // a row without keys: every exponent is -inf
         const uint64_t neg2 = f2(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
-        {
-          uint32_t v[2][32];
-          tmem_ld32_async(tS, v[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&u)[32] = v[c & 1];
-            tmem_ld_wait(u);
-            // P of chunk c overwrites columns [16 c, 16 c + 16), whose scores (of chunks 0 and 1)
-            // have been loaded
-            if (c < 3) tmem_ld32_async(tS + 32 * (c + 1), v[(c + 1) & 1]);
-            if (w[c] == 0u) {
-              tmem_st16_zero(tS + 16 * c);
-            } else {
-              if (w[c] != ~0u) {
+        for (int c = 0; c < 4; ++c) {
+          if (w[c] == 0u) {  // no key in this chunk: no exponentials
+            tmem_st16_zero(tS + 16 * c);
+          } else {
+            uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((w[c] >> e) & 1u)) u[e] = 0xff800000u;
-              }
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const uint64_t z = ffma2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), c2x2, neg2);
-                const float p0 = ex2_approx(f2_lo(z)), p1 = ex2_approx(f2_hi(z));
-                sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], f2(p0, p1));
-                p[e >> 1] = pack_bf16x2(p0, p1);
-              }
-              tmem_st16(tS + 16 * c, p);
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t z = ffma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), c2x2, neg2);
+              const float p0 = ex2_approx(f2_lo(z)), p1 = ex2_approx(f2_hi(z));
+              sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], f2(p0, p1));
+              p[e >> 1] = pack_bf16x2(p0, p1);
             }
-            if (c & 1) {
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[(c == 1 ? Lay::PF : Lay::PF2) + x]);
-            }
+            tmem_st16(tS + 16 * c, p);
+          }
+          if (c & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[(c == 1 ? Lay::PF : Lay::PF2) + x]);
           }
         }
         const uint64_t s2 = fadd2(sum[0], sum[1]);
