@@ -32,10 +32,6 @@
 namespace sq {
 
 constexpr int kCrossThreads = 512;
-// Registers per thread: the eight softmax warps hold a whole row of scores (128), the others
-// need few. 256 * 184 + 256 * 72 = 512 * 128, the block's share at launch.
-constexpr int kCrossSoftmaxRegs = 184, kCrossOtherRegs = 72;
-
 struct alignas(64) CrossMaps {
   CUtensorMap q, k, v, o;
 };
@@ -63,23 +59,14 @@ struct CrossFwdLayout {
   static constexpr int INV_OFF = KV_OFF + NKV * TILE;  // [job][parity][128] 1 / sum
   static constexpr int BAR_OFF = INV_OFF + 4 * 128 * 4;
   static constexpr int QF = 0, QE = NQ, KVF = 2 * NQ, KVE = KVF + NKV, RDY = KVE + NKV, SF = RDY + NKV, PF = SF + 2,
-                       PF2 = PF + 2, OF = PF2 + 2, OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 1, NBAR = DRAIN + 1;
+                       OF = PF + 4, OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 1, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
-// The order of a CTA's key and value tiles: the walk that the loader, the masker and the MMA
-// issuer share. on_pv(x, e, first, last, free): P V of job x's pending block, values at ring
-// entry e (new: this is the entry's first use; free: its last). on_s(x, e, new, free, it, r, k)
-// likewise for the scores of block k.
-struct CrossWalk {
-  uint32_t entries = 0;
-  uint32_t cur_k = 0, cur_v = 0;
-  bool pend[2] = {false, false}, pend_first[2], pend_last[2], pend_new[2], pend_free[2];
-  int pend_kb[2];
-  CrossItem pend_it[2];
-  int pend_limit[2];
-};
+// What a visitor of the walk (below) is told about a product: the ring entry it reads is new,
+// is done with, and the product is its job's first or last.
+enum { CW_NEW = 1, CW_DONE = 2, CW_FIRST = 4, CW_LAST = 8 };
 
 template <int D, bool MASKED>
 __global__ void __launch_bounds__(kCrossThreads, 1)
@@ -111,8 +98,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[Lay::SF + i], 1);
-      mbar_init(&bars[Lay::PF + i], 4);
-      mbar_init(&bars[Lay::PF2 + i], 4);
+      mbar_init(&bars[Lay::PF + i], 4);      // keys 0-63 of P
+      mbar_init(&bars[Lay::PF + 2 + i], 4);  // keys 64-127
       mbar_init(&bars[Lay::OF + i], 1);
       mbar_init(&bars[Lay::OE + i], 4);
       mbar_init(&bars[Lay::LF + 2 * i], 4);
@@ -149,67 +136,91 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     }
     return len_v;
   };
-  // Walks the CTA's products in issue order; stops when a visitor returns false.
-  auto walk = [&](auto&& on_pv, auto&& on_s) -> bool {
-    CrossWalk w;
-    auto flush = [&](int x) -> bool {
-      if (!w.pend[x]) return true;
-      w.pend[x] = false;
-      if (w.pend_new[x]) w.cur_v = w.entries++;
-      return on_pv(x, w.cur_v, w.pend_new[x], w.pend_free[x], w.pend_first[x], w.pend_last[x], w.pend_it[x],
-                   w.pend_kb[x], w.pend_limit[x]);
-    };
-    for (int i = blockIdx.x; i < plan.items; i += gridDim.x) {
-      const CrossItem it = cross_item(plan, args.heads, i);
-      const int len = len_of(it.b);
-      const CrossRange r0 = cross_range(plan, len, it.sp[0]);
-      const CrossRange r1 = it.qt[1] < 0 ? CrossRange{0, 0, 0} : cross_range(plan, len, it.sp[1]);
-      const int nk = r0.nk > r1.nk ? r0.nk : r1.nk;
+  // The order of a CTA's products, which the loader, the masker and the MMA issuer share:
+  // on_item(item, ranges of its two jobs), then for every block k and job x on_pv(x, entry,
+  // flags) of the job's block before, if any, and on_s(x, entry, flags, k). entry counts the
+  // key and value tiles in that order. Stops when a visitor returns false. The loops are not
+  // unrolled: the code of a role is fetched once.
+  auto walk = [&](auto&& on_item, auto&& on_pv, auto&& on_s) -> bool {
+    uint32_t entries = 0, cur_k = 0, cur_v = 0;
+    uint32_t pend = 0;  // flags of the job's block whose P V is still to come (16: there is one), 8 bits per job
+#pragma unroll 1
+    for (int i = blockIdx.x;; i += gridDim.x) {
+      const bool more = i < plan.items;
+      int nk0 = 0, nk1 = 0;
+      bool shared = false;
+      if (more) {
+        const CrossItem it = cross_item(plan, args.heads, i);
+        const int len = len_of(it.b);
+        const CrossRange r0 = cross_range(plan, len, it.sp[0]);
+        CrossRange r1 = r0;
+        if (it.qt[1] < 0)
+          r1.nk = 0;
+        else if (!it.shared)
+          r1 = cross_range(plan, len, it.sp[1]);
+        nk0 = r0.nk;
+        nk1 = r1.nk;
+        shared = it.shared;
+        on_item(it, r0, r1);
+      }
+      const int nk = more ? (nk0 > nk1 ? nk0 : nk1) : 1;
+#pragma unroll 1
       for (int k = 0; k < nk; ++k) {
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          if (!flush(x)) return false;
-          const CrossRange& r = x ? r1 : r0;
-          if (k >= r.nk) continue;
-          const bool fresh = !it.shared || x == 0, done = !it.shared || x == 1;
-          if (fresh) w.cur_k = w.entries++;
-          if (!on_s(x, w.cur_k, fresh, done, k == 0, it, r.k0 + k, r.limit)) return false;
-          w.pend[x] = true;
-          w.pend_new[x] = fresh;
-          w.pend_free[x] = done;
-          w.pend_first[x] = k == 0;
-          w.pend_last[x] = k == r.nk - 1;
-          w.pend_it[x] = it;
-          w.pend_kb[x] = r.k0 + k;
-          w.pend_limit[x] = r.limit;
+          const uint32_t f = (pend >> (8 * x)) & 255u;
+          if (f) {
+            pend &= ~(255u << (8 * x));
+            if (f & CW_NEW) cur_v = entries++;
+            if (!on_pv(x, cur_v, f)) return false;
+          }
+          const int nkx = x ? nk1 : nk0;
+          if (k >= nkx) continue;
+          const uint32_t g = (shared ? (x ? CW_DONE : CW_NEW) : (CW_DONE | CW_NEW)) | (k == 0 ? CW_FIRST : 0) |
+                             (k == nkx - 1 ? CW_LAST : 0);
+          if (g & CW_NEW) cur_k = entries++;
+          if (!on_s(x, cur_k, g, k)) return false;
+          pend |= (g | 16u) << (8 * x);
         }
       }
+      if (!more) return true;
     }
-    return flush(0) && flush(1);
   };
 
   if (warp >= 12) {
-    regs_give<kCrossOtherRegs>();
     if (warp == 12) {
-      // ================================================================ key and value loads
+      // ============================================================== key and value loads
       if (lane == 0) {
         uint32_t issued = 0;
-        auto load = [&](uint32_t e, const CUtensorMap* m, int h, int b, int kb) -> bool {
+        int kh = 0, kb = 0, vh = 0, vb = 0, k0[2] = {0, 0};
+        int pvh[2], pvb[2], prow[2];  // head, batch and first row of each job's pending value tile
+        auto load = [&](uint32_t e, const CUtensorMap* m, int row, int h, int b) -> bool {
           const uint32_t s = e % Lay::NKV;
-          if (!mbar_wait_inline(&bars[Lay::KVE + s], ((e / Lay::NKV) & 1) ^ 1, abort_flag, to)) return false;
+          if (!mbar_wait(&bars[Lay::KVE + s], ((e / Lay::NKV) & 1) ^ 1, abort_flag, to)) return false;
           mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, kb * 128, h, b);
+            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
           issued = e + 1;
           return true;
         };
         walk(
-            [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int) -> bool {
-              return !fresh || load(e, &maps.v, it.hk * args.v_h, it.b * args.v_b, kb);
+            [&](const CrossItem& it, const CrossRange& r0, const CrossRange& r1) {
+              kh = it.hk * args.k_h;
+              kb = it.b * args.k_b;
+              vh = it.hk * args.v_h;
+              vb = it.b * args.v_b;
+              k0[0] = r0.k0;
+              k0[1] = r1.k0;
             },
-            [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int) -> bool {
-              return !fresh || load(e, &maps.k, it.hk * args.k_h, it.b * args.k_b, kb);
+            [&](int x, uint32_t e, uint32_t f) -> bool {
+              return !(f & CW_NEW) || load(e, &maps.v, prow[x], pvh[x], pvb[x]);
+            },
+            [&](int x, uint32_t e, uint32_t f, int k) -> bool {
+              prow[x] = (k0[x] + k) * 128;
+              pvh[x] = vh;
+              pvb[x] = vb;
+              return !(f & CW_NEW) || load(e, &maps.k, prow[x], kh, kb);
             });
         // let every issued load land before the CTA may exit
         for (uint32_t s = 0; s < uint32_t(Lay::NKV); ++s) {
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           for (int x = 0; ok && x < 2; ++x) {
             if (it.qt[x] < 0) continue;
             const uint32_t s = q % Lay::NQ;
-            if (!(ok = mbar_wait_inline(&bars[Lay::QE + s], ((q / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
+            if (!(ok = mbar_wait(&bars[Lay::QE + s], ((q / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
             mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
 #pragma unroll
             for (int c = 0; c < DH; ++c)
@@ -244,14 +255,16 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     } else if (warp == 14) {
       // ================================================================ masked rows to zero
       if (MASKED) {
-        auto fix = [&](uint32_t e, const CrossItem& it, int kb, int limit, bool zero) -> bool {
+        int b = 0, pb[2], prow[2], plim[2], k0[2], lim[2];
+        // zero: value tiles; masked scores are replaced, so key tiles stay as they are
+        auto fix = [&](uint32_t e, int b, int row, int limit, bool zero) -> bool {
           const uint32_t s = e % Lay::NKV;
-          const bool ok = mbar_wait_inline(&bars[Lay::KVF + s], (e / Lay::NKV) & 1, abort_flag, to);
+          const bool ok = mbar_wait(&bars[Lay::KVF + s], (e / Lay::NKV) & 1, abort_flag, to);
           if (!__all_sync(0xffffffffu, ok)) return false;
           if (zero) {
             uint32_t w[4];
-            block_words(limit - kb * 128,
-                        args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + kb * 128, lane, w);
+            block_words(limit - row, args.mask.keys == nullptr ? nullptr : args.mask.keys + b * args.mask.stride + row,
+                        lane, w);
             zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
             __syncwarp();
           }
@@ -259,83 +272,95 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           return true;
         };
         walk(
-            [&](int, uint32_t e, bool fresh, bool, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
-              return !fresh || fix(e, it, kb, limit, true);
+            [&](const CrossItem& it, const CrossRange& r0, const CrossRange& r1) {
+              b = it.b;
+              k0[0] = r0.k0;
+              k0[1] = r1.k0;
+              lim[0] = r0.limit;
+              lim[1] = r1.limit;
             },
-            [&](int, uint32_t e, bool fresh, bool, bool, const CrossItem& it, int kb, int limit) -> bool {
-              return !fresh || fix(e, it, kb, limit, false);  // masked scores are replaced, not multiplied
+            [&](int x, uint32_t e, uint32_t f) -> bool {
+              return !(f & CW_NEW) || fix(e, pb[x], prow[x], plim[x], true);
+            },
+            [&](int x, uint32_t e, uint32_t f, int k) -> bool {
+              pb[x] = b;
+              prow[x] = (k0[x] + k) * 128;
+              plim[x] = lim[x];
+              return !(f & CW_NEW) || fix(e, b, prow[x], plim[x], false);
             });
       }
     } else if (warp == 13) {
-      // ================================================================ MMA issuer
+      // ============================================================== MMA issuer
       if (lane == 0) {
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
         constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
-        uint32_t qn = 0;                    // query tiles taken
-        uint32_t blocks[2] = {0, 0};        // P V products issued per job slot
-        uint32_t jobs[2] = {0, 0};          // jobs begun per job slot
-        uint32_t qslot[2] = {0, 0};
-        walk(
-            [&](int x, uint32_t e, bool, bool done, bool first, bool last, const CrossItem&, int, int) -> bool {
-              const uint32_t s = e % Lay::NKV, par = blocks[x] & 1;
-              if (!mbar_wait_inline(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-              // the job's first product overwrites O: the epilogue has drained the last job's
-              if (first) {
-                if (jobs[x] > 0 && !mbar_wait_inline(&bars[Lay::OE + x], (jobs[x] - 1) & 1, abort_flag, to)) return false;
-                ++jobs[x];
-              }
-              if (!mbar_wait_inline(&bars[Lay::PF + x], par, abort_flag, to)) return false;
-              tc_fence_after();
-              const uint32_t va = sbase + Lay::KV_OFF + s * Lay::TILE;
-              const uint32_t o = tmem + 256 + D * x, p = tmem + 128 * x;
+        const uint64_t q0 = sdesc_sw128(sbase + Lay::Q_OFF, 16, 1024), k0 = sdesc_sw128(sbase + Lay::KV_OFF, 16, 1024),
+                       v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024);
+        uint32_t qn = 0;                  // query tiles taken
+        uint32_t qslot = 0;               // query slot of each job, 8 bits each
+        uint32_t par = 0, jpar = 0;       // bit x: parity of job slot x's P V products, of its jobs
+        uint32_t begun = 0;               // bit x: job slot x has begun a job
+        walk([](const CrossItem&, const CrossRange&, const CrossRange&) {},
+             [&](int x, uint32_t e, uint32_t f) -> bool {
+               const uint32_t s = e % Lay::NKV, p = (par >> x) & 1;
+               if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
+               // the job's first product overwrites O: the epilogue has drained the last job's
+               if (f & CW_FIRST) {
+                 if (((begun >> x) & 1) && !mbar_wait(&bars[Lay::OE + x], ((jpar >> x) & 1) ^ 1, abort_flag, to))
+                   return false;
+                 begun |= 1u << x;
+                 jpar ^= 1u << x;
+               }
+               if (!mbar_wait(&bars[Lay::PF + x], p, abort_flag, to)) return false;
+               tc_fence_after();
+               const uint64_t va = v0 + s * (Lay::TILE >> 4);
+               const uint32_t o = tmem + 256 + D * x, a = tmem + 128 * x;
+               mma_ts(o, a, va, id_o, f & CW_FIRST ? 0u : 1u);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, (!first || kk > 0) ? 1u : 0u);
-              if (!mbar_wait_inline(&bars[Lay::PF2 + x], par, abort_flag, to)) return false;
-              tc_fence_after();
+               for (int kk = 1; kk < 4; ++kk) mma_ts(o, a + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+               if (!mbar_wait(&bars[Lay::PF + 2 + x], p, abort_flag, to)) return false;
+               tc_fence_after();
 #pragma unroll
-              for (int kk = 4; kk < 8; ++kk)
-                mma_ts(o, p + kk * 8, sdesc_sw128(va + kk * 2048, kCrossBlk, 1024), id_o, 1u);
-              if (done) tc_commit(&bars[Lay::KVE + s]);
-              if (last) tc_commit(&bars[Lay::OF + x]);
-              ++blocks[x];
-              return true;
-            },
-            [&](int x, uint32_t e, bool, bool done, bool first, const CrossItem&, int, int) -> bool {
-              const uint32_t s = e % Lay::NKV;
-              if (!mbar_wait_inline(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-              if (first) {
-                qslot[x] = qn % Lay::NQ;
-                if (!mbar_wait_inline(&bars[Lay::QF + qslot[x]], (qn / Lay::NQ) & 1, abort_flag, to)) return false;
-                ++qn;
-              }
-              tc_fence_after();
-              // S overwrites the columns that this job's previous P V reads P from: the tensor
-              // core runs the products of one thread in issue order
-              const uint32_t qa = sbase + Lay::Q_OFF + qslot[x] * Lay::TILE, ka = sbase + Lay::KV_OFF + s * Lay::TILE;
+               for (int kk = 4; kk < 8; ++kk) mma_ts(o, a + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+               if (f & CW_DONE) tc_commit(&bars[Lay::KVE + s]);
+               if (f & CW_LAST) tc_commit(&bars[Lay::OF + x]);
+               par ^= 1u << x;
+               return true;
+             },
+             [&](int x, uint32_t e, uint32_t f, int) -> bool {
+               const uint32_t s = e % Lay::NKV;
+               if (f & CW_FIRST) {
+                 const uint32_t z = qn % Lay::NQ;
+                 if (!mbar_wait(&bars[Lay::QF + z], (qn / Lay::NQ) & 1, abort_flag, to)) return false;
+                 qslot = x ? (qslot & 0xffu) | (z << 8) : (qslot & 0xff00u) | z;
+                 ++qn;
+               }
+               if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
+               tc_fence_after();
+               // S overwrites the columns that this job's previous P V reads P from: the tensor
+               // core runs the products of one thread in issue order
+               const uint64_t qa = q0 + ((qslot >> (8 * x)) & 255u) * (Lay::TILE >> 4), ka = k0 + s * (Lay::TILE >> 4);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-                mma_ss(tmem + 128 * x, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_s,
-                       kk > 0 ? 1u : 0u);
-              }
-              tc_commit(&bars[Lay::SF + x]);
-              if (done) tc_commit(&bars[Lay::KVE + s]);
-              return true;
-            });
+               for (int kk = 0; kk < D / 16; ++kk) {
+                 const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+                 mma_ss(tmem + 128 * x, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
+               }
+               tc_commit(&bars[Lay::SF + x]);
+               if (f & CW_DONE) tc_commit(&bars[Lay::KVE + s]);
+               return true;
+             });
         tc_commit(&bars[Lay::DRAIN]);
         mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
       }
     }
   } else if (warp >= 8) {
     // ================================================================ epilogue
-    regs_give<kCrossOtherRegs>();
     const int row = threadIdx.x & 127;
     uint32_t q = 0, jobs[2] = {0, 0};
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
     };
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           mbar_arrive(&bars[Lay::ST]);
         }
         if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = mbar_wait_inline(&bars[Lay::ST], (q - 1) & 1, abort_flag, to);
+          ok = mbar_wait(&bars[Lay::ST], (q - 1) & 1, abort_flag, to);
 #pragma unroll
           for (int c = 0; ok && c < DH; ++c)
             tma_store_4d(&maps.o, sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, c * 64, it.qt[x] * 128,
@@ -415,7 +440,6 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     }
   } else {
     // ================================================================ softmax
-    regs_take<kCrossSoftmaxRegs>();
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + 128 * x;
     const uint32_t tO = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
@@ -424,7 +448,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     uint32_t sc = 0, jobs = 0;
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
     };
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
@@ -448,31 +472,38 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           tc_fence_before();
           if (lane == 0) {
             mbar_arrive(&bars[Lay::PF + x]);
-            mbar_arrive(&bars[Lay::PF2 + x]);
+            mbar_arrive(&bars[Lay::PF + 2 + x]);
           }
           continue;
         }
-        // ---- row maximum; masked scores become -inf
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait(v[c]);
-          if (w[c] != ~0u) {
+        // a block that does not count whole: its masked scores become -inf where they lie
+        if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t word = c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
+            if (word == ~0u) continue;
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * c, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!((w[c] >> e) & 1u)) v[c][e] = 0xff800000u;
+              if (!((word >> e) & 1u)) v[e] = 0xff800000u;
+            tmem_st32(tS + 32 * c, v);
           }
-          float a[4];
+          tmem_st_wait();
+        }
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[64];
+          tmem_ld64(tS + 64 * c, v);
+          float a[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[j] = fmaxf(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 4]));
+          for (int j = 0; j < 8; ++j) a[j] = fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 8]));
 #pragma unroll
-          for (int e = 8; e < 32; e += 8)
+          for (int e = 16; e < 64; e += 16)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] = fmax3(a[j], __uint_as_float(v[c][e + j]), __uint_as_float(v[c][e + j + 4]));
-          mx = fmax3(mx, fmax3(a[0], a[1], a[2]), a[3]);
+            for (int j = 0; j < 8; ++j) a[j] = fmax3(a[j], __uint_as_float(v[e + j]), __uint_as_float(v[e + j + 8]));
+          mx = fmax3(fmax3(mx, a[0], a[1]), fmax3(a[2], a[3], a[4]), fmax3(a[5], a[6], a[7]));
         }
         // the first block sets the maximum; a later one moves it only when it grows by more
         // than 2^8 (then O and the sum are rescaled), else its probabilities may exceed 1
@@ -497,27 +528,28 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         const float neg = m_use == -INFINITY ? 0.f : -m_use * c2;  // a row without keys: every exponent is -inf
         const uint64_t neg2 = f2(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (w[c] == 0u) {  // no key in this chunk: no exponentials
-            tmem_st16_zero(tS + 16 * c);
+        // P of 64 keys at a time, packed over columns [32 c, 32 c + 32), whose scores are done with
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          if ((c ? w[2] | w[3] : w[0] | w[1]) == 0u) {  // no key counts: no exponentials
+            tmem_st16_zero(tS + 32 * c);
+            tmem_st16_zero(tS + 32 * c + 16);
           } else {
-            uint32_t p[16];
+            uint32_t v[64], p[32];
+            tmem_ld64(tS + 64 * c, v);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t z = ffma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), c2x2, neg2);
+            for (int e = 0; e < 64; e += 2) {
+              const uint64_t z = ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg2);
               const float p0 = ex2_approx(f2_lo(z)), p1 = ex2_approx(f2_hi(z));
               sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], f2(p0, p1));
               p[e >> 1] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(tS + 16 * c, p);
+            tmem_st32(tS + 32 * c, p);
           }
-          if (c & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[(c == 1 ? Lay::PF : Lay::PF2) + x]);
-          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::PF + 2 * c + x]);
         }
         const uint64_t s2 = fadd2(sum[0], sum[1]);
         l_run = l_run * alpha + (f2_lo(s2) + f2_hi(s2));
