@@ -193,7 +193,8 @@ squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& ma
   static std::atomic<bool> done[kMaxDevices];
   squad_status s = allow_smem(kern, Lay::BYTES, dev, done);
   if (s != SQUAD_OK) return s;
-  const int grid = a.plan.items < dev.sms ? a.plan.items : dev.sms;
+  // split keys: one item per CTA (the kernel uses the room of a second item's queries)
+  const int grid = a.plan.items < dev.sms || a.plan.splits > 1 ? a.plan.items : dev.sms;
   kern<<<grid, sq::kCrossThreads, Lay::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
   return SQUAD_OK;

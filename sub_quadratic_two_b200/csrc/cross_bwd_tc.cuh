@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 14) {  // a warp whose lanes stay together: TMEM is taken and given back by whole warps
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
+        mbar_arrive(&bars[Lay::ST]);  // before OE, which the next tile's arrivals at ST wait for
         mbar_arrive(&bars[Lay::OE]);
-        mbar_arrive(&bars[Lay::ST]);
       }
       if (threadIdx.x == 256) {
         ok = mbar_wait(&bars[Lay::ST], job & 1, abort_flag, to);
@@ -474,9 +474,11 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     }
   }
 
+  __syncwarp();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0 && args.err != nullptr) atomicCAS(args.err, 0, 1);
-  if (warp == 13) {
+  if (warp == 14) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 14) {  // a warp whose lanes stay together: TMEM is taken and given back by whole warps
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -784,9 +786,8 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t v[32];
-          if (any) {
-            tmem_ld32(acc + c, v);
-          }
+          __syncwarp();  // lanes part below: TMEM is read by whole warps
+          if (any) tmem_ld32(acc + c, v);
           // keys that do not count get zeros, whatever the accumulator holds
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = live ? __float_as_uint(__uint_as_float(v[e]) * sc) : 0u;
@@ -902,9 +903,11 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     }
   }
 
+  __syncwarp();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0 && args.err != nullptr) atomicCAS(args.err, 0, 1);
-  if (warp == 13) {
+  if (warp == 14) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -8,16 +8,19 @@
 // Roles (512 threads):
 //   warps 0-3, 4-7  softmax of job 0, job 1 (thread = query row = TMEM lane)
 //   warps 8-11      epilogue: O / sum -> bf16 -> the job's Q tile (no longer needed) in shared
-//                   memory -> TMA store, so the softmax warps go on with the next item
-//   warp 12         TMA loads of key and value tiles, one ring in consumption order
-//   warp 13         one thread issues every tcgen05.mma
-//   warp 14         masks: zeroes the masked rows of key and value tiles before they are used
-//                   (what lies there may be NaN or infinite, and P = 0 times NaN is NaN)
-//   warp 15         TMA loads of query tiles (four slots: an item ahead)
+//                   memory -> TMA store, so the softmax warps go on with the next item; their
+//                   first thread then loads the job's query tile of the item after next there
+//   warp 12         TMA loads of key and value tiles, K(0) V(0) K(1) V(1) ... in a ring (a ring for
+//                   each job where the keys are split)
+//   warps 13, 15    one thread each issues the tcgen05.mma of job 0, job 1: what a thread spends
+//                   between its products (waits, addresses: some 100 cycles each) passes under
+//                   the products of the other
+//   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies
+//                   there may be NaN or infinite, and P = 0 times NaN is NaN)
 // TMEM (512 columns): S of job x at [128x, 128x+128), O at [256 + D x, ...). P overwrites S in
 // place as packed bf16 and goes to the tensor core in two halves of 64 keys.
-// The order of the products is S0(0) S1(0) | PV0(0) S0(1) | PV1(0) S1(1) | ...: while the
-// tensor core works on one job, the other job's softmax runs.
+// Each job's products run S(0) | PV(0) S(1) | PV(1) S(2) | ...; while the tensor core works on
+// one job, the other job's softmax runs.
 // A block of 128 x 128 costs the tensor core 4 x 128 x 128 x D flops (1,024 cycles at D = 128)
 // and the multi-function unit 128 x 128 exponentials (1,024 cycles at 16 a cycle): both are
 // near their limit at once.
@@ -52,21 +55,19 @@ struct CrossFwdArgs {
 template <int D>
 struct CrossFwdLayout {
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NQ = 4;
-  static constexpr int NKV = D == 128 ? 3 : 8;
-  static constexpr int Q_OFF = 0;
-  static constexpr int KV_OFF = NQ * TILE;
-  static constexpr int INV_OFF = KV_OFF + NKV * TILE;  // [job][parity][128] 1 / sum
-  static constexpr int BAR_OFF = INV_OFF + 4 * 128 * 4;
-  static constexpr int QF = 0, QE = NQ, KVF = 2 * NQ, KVE = KVF + NKV, RDY = KVE + NKV, SF = RDY + NKV, PF = SF + 2,
-                       OF = PF + 4, OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 1, NBAR = DRAIN + 1;
+  static constexpr int NQ = 4;  // query tile of job x of the CTA's j-th item: slot 2 (j & 1) + x
+  static constexpr int NKV = D == 128 ? 3 : 8;  // ring of key and value tiles, behind the query tiles
+  // Split keys: a CTA has one item, so query slots 2 and 3 are free, and each job takes half of
+  // the tiles behind slot 1 as a ring of its own. (With one ring for both, an issuer would not
+  // see the phases of the tiles that the other job reads, and a wait by parity needs every phase.)
+  static constexpr int NS = (NKV + 2) / 2;
+  static constexpr int NB = NKV > 2 * NS ? NKV : 2 * NS;  // ring barriers of each kind
+  static constexpr int BAR_OFF = (NQ + NKV) * TILE;
+  static constexpr int QF = 0, KVF = QF + NQ, KVE = KVF + NB, RDY = KVE + NB, SF = RDY + NB, PF = SF + 2, OF = PF + 4,
+                       OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 2, NBAR = DRAIN + 2;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
-
-// What a visitor of the walk (below) is told about a product: the ring entry it reads is new,
-// is done with, and the product is its job's first or last.
-enum { CW_NEW = 1, CW_DONE = 2, CW_FIRST = 4, CW_LAST = 8 };
 
 template <int D, bool MASKED>
 __global__ void __launch_bounds__(kCrossThreads, 1)
@@ -77,7 +78,6 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
-  float* inv_sum = reinterpret_cast<float*>(smem + Lay::INV_OFF);
   const CrossPlan& plan = args.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t to = args.timeout_ns;
@@ -87,30 +87,17 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Lay::NQ; ++i) {
-      mbar_init(&bars[Lay::QF + i], 1);
-      mbar_init(&bars[Lay::QE + i], 1);
+    for (int i = 0; i < Lay::NBAR; ++i) {
+      // key and value tiles are released by both issuers (or twice by the only one that reads
+      // them); the softmax and epilogue warps arrive one by one
+      const int count = i >= Lay::KVE && i < Lay::RDY ? 2
+                        : (i >= Lay::PF && i < Lay::OF) || (i >= Lay::OE && i < Lay::DRAIN) ? 4 : 1;
+      mbar_init(&bars[i], count);
     }
-    for (int i = 0; i < Lay::NKV; ++i) {
-      mbar_init(&bars[Lay::KVF + i], 1);
-      mbar_init(&bars[Lay::KVE + i], 1);
-      mbar_init(&bars[Lay::RDY + i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[Lay::SF + i], 1);
-      mbar_init(&bars[Lay::PF + i], 4);      // keys 0-63 of P
-      mbar_init(&bars[Lay::PF + 2 + i], 4);  // keys 64-127
-      mbar_init(&bars[Lay::OF + i], 1);
-      mbar_init(&bars[Lay::OE + i], 4);
-      mbar_init(&bars[Lay::LF + 2 * i], 4);
-      mbar_init(&bars[Lay::LF + 2 * i + 1], 4);
-    }
-    mbar_init(&bars[Lay::ST], 4);
-    mbar_init(&bars[Lay::DRAIN], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 14) {  // a warp whose lanes stay together: TMEM is taken and given back by whole warps
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -126,6 +113,18 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   const uint32_t tmem = *tmem_holder;
   const uint32_t sbase = smem_u32(smem);
 
+  // Rings of key and value tiles: entry n of job x (or of both) lies in slot(x, n), for the
+  // use(n)-th time.
+  struct Ring {
+    uint32_t size, tile0;
+    int count;
+    __device__ __forceinline__ uint32_t slot(int x, uint32_t n) const {
+      return (count == 2 ? x * size : 0u) + n % size;
+    }
+    __device__ __forceinline__ uint32_t use(uint32_t n) const { return n / size; }
+  };
+  const Ring ring = plan.splits > 1 ? Ring{uint32_t(Lay::NS), 2u, 2} : Ring{uint32_t(Lay::NKV), uint32_t(Lay::NQ), 1};
+
   // Keys of batch row b that may count (the same row is asked for many times in a row).
   int len_b = -1, len_v = 0;
   auto len_of = [&](int b) -> int {
@@ -136,252 +135,235 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     }
     return len_v;
   };
-  // The order of a CTA's products, which the loader, the masker and the MMA issuer share:
-  // on_item(item, ranges of its two jobs), then for every block k and job x on_pv(x, entry,
-  // flags) of the job's block before, if any, and on_s(x, entry, flags, k). entry counts the
-  // key and value tiles in that order. Stops when a visitor returns false. The loops are not
-  // unrolled: the code of a role is fetched once.
-  auto walk = [&](auto&& on_item, auto&& on_pv, auto&& on_s) -> bool {
-    uint32_t entries = 0, cur_k = 0, cur_v = 0;
-    uint32_t pend = 0;  // flags of the job's block whose P V is still to come (16: there is one), 8 bits per job
-#pragma unroll 1
-    for (int i = blockIdx.x;; i += gridDim.x) {
-      const bool more = i < plan.items;
-      int nk0 = 0, nk1 = 0;
-      bool shared = false;
-      if (more) {
-        const CrossItem it = cross_item(plan, args.heads, i);
-        const int len = len_of(it.b);
-        const CrossRange r0 = cross_range(plan, len, it.sp[0]);
-        CrossRange r1 = r0;
-        if (it.qt[1] < 0)
-          r1.nk = 0;
-        else if (!it.shared)
-          r1 = cross_range(plan, len, it.sp[1]);
-        nk0 = r0.nk;
-        nk1 = r1.nk;
-        shared = it.shared;
-        on_item(it, r0, r1);
-      }
-      const int nk = more ? (nk0 > nk1 ? nk0 : nk1) : 1;
-#pragma unroll 1
-      for (int k = 0; k < nk; ++k) {
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t f = (pend >> (8 * x)) & 255u;
-          if (f) {
-            pend &= ~(255u << (8 * x));
-            if (f & CW_NEW) cur_v = entries++;
-            if (!on_pv(x, cur_v, f)) return false;
-          }
-          const int nkx = x ? nk1 : nk0;
-          if (k >= nkx) continue;
-          const uint32_t g = (shared ? (x ? CW_DONE : CW_NEW) : (CW_DONE | CW_NEW)) | (k == 0 ? CW_FIRST : 0) |
-                             (k == nkx - 1 ? CW_LAST : 0);
-          if (g & CW_NEW) cur_k = entries++;
-          if (!on_s(x, cur_k, g, k)) return false;
-          pend |= (g | 16u) << (8 * x);
-        }
-      }
-      if (!more) return true;
-    }
-  };
-
   if (warp >= 12) {
     if (warp == 12) {
       // ============================================================== key and value loads
       if (lane == 0) {
-        uint32_t issued = 0;
-        int kh = 0, kb = 0, vh = 0, vb = 0, k0[2] = {0, 0};
-        int pvh[2], pvb[2], prow[2];  // head, batch and first row of each job's pending value tile
-        auto load = [&](uint32_t e, const CUtensorMap* m, int row, int h, int b) -> bool {
-          const uint32_t s = e % Lay::NKV;
-          if (!mbar_wait(&bars[Lay::KVE + s], ((e / Lay::NKV) & 1) ^ 1, abort_flag, to)) return false;
+        uint32_t e[2] = {0, 0};
+        auto load = [&](int x, const CUtensorMap* m, int row, int h, int b) -> bool {
+          const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
+          if (!mbar_wait(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
           mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
-          issued = e + 1;
+            tma_load_4d(sbase + (ring.tile0 + s) * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
+          x ? ++e[1] : ++e[0];
           return true;
         };
-        walk(
-            [&](const CrossItem& it, const CrossRange& r0, const CrossRange& r1) {
-              kh = it.hk * args.k_h;
-              kb = it.b * args.k_b;
-              vh = it.hk * args.v_h;
-              vb = it.b * args.v_b;
-              k0[0] = r0.k0;
-              k0[1] = r1.k0;
-            },
-            [&](int x, uint32_t e, uint32_t f) -> bool {
-              return !(f & CW_NEW) || load(e, &maps.v, prow[x], pvh[x], pvb[x]);
-            },
-            [&](int x, uint32_t e, uint32_t f, int k) -> bool {
-              prow[x] = (k0[x] + k) * 128;
-              pvh[x] = vh;
-              pvb[x] = vb;
-              return !(f & CW_NEW) || load(e, &maps.k, prow[x], kh, kb);
-            });
-        // let every issued load land before the CTA may exit
-        for (uint32_t s = 0; s < uint32_t(Lay::NKV); ++s) {
-          const uint32_t uses = issued > s ? (issued - s + Lay::NKV - 1) / Lay::NKV : 0;
-          if (uses) mbar_wait_drain(&bars[Lay::KVF + s], (uses - 1) & 1, to);
-        }
-      }
-    } else if (warp == 15) {
-      // ================================================================ query loads
-      if (lane == 0) {
-        uint32_t q = 0;
         bool ok = true;
         for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
           const CrossItem it = cross_item(plan, args.heads, i);
-          for (int x = 0; ok && x < 2; ++x) {
-            if (it.qt[x] < 0) continue;
-            const uint32_t s = q % Lay::NQ;
-            if (!(ok = mbar_wait(&bars[Lay::QE + s], ((q / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
-            mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
-#pragma unroll
-            for (int c = 0; c < DH; ++c)
-              tma_load_4d(sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + s], c * 64,
-                          it.qt[x] * 128, it.h * args.q_h, it.b * args.q_b);
-            ++q;
-          }
+          const CrossRange r = cross_range(plan, len_of(it.b), it.sp[0]);
+          const int kh = it.hk * args.k_h, kb = it.b * args.k_b, vh = it.hk * args.v_h, vb = it.b * args.v_b;
+          // values of block k - 1, then keys of block k
+          for (int k = 0; ok && k <= r.nk; ++k)
+            for (int x = 0; ok && x < ring.count; ++x) {
+              const int row = (r.k0 + x * r.nk + k) * 128;
+              if (k > 0) ok = load(x, &maps.v, row - 128, vh, vb);
+              if (ok && k < r.nk) ok = load(x, &maps.k, row, kh, kb);
+            }
         }
-        for (uint32_t s = 0; s < uint32_t(Lay::NQ); ++s) {
-          const uint32_t uses = q > s ? (q - s + Lay::NQ - 1) / Lay::NQ : 0;
-          if (uses) mbar_wait_drain(&bars[Lay::QF + s], (uses - 1) & 1, to);
+        // let every issued load land before the CTA may exit
+        for (int x = 0; x < ring.count; ++x) {
+          const uint32_t n = x ? e[1] : e[0];
+          for (uint32_t s = 0; s < ring.size; ++s)
+            if (n > s) mbar_wait_drain(&bars[Lay::KVF + x * ring.size + s], ((n - 1 - s) / ring.size) & 1, to);
         }
       }
     } else if (warp == 14) {
-      // ================================================================ masked rows to zero
+      // ============================================================== masked value rows to zero
       if (MASKED) {
-        int b = 0, pb[2], prow[2], plim[2], k0[2], lim[2];
-        // zero: value tiles; masked scores are replaced, so key tiles stay as they are
-        auto fix = [&](uint32_t e, int b, int row, int limit, bool zero) -> bool {
-          const uint32_t s = e % Lay::NKV;
-          const bool ok = mbar_wait(&bars[Lay::KVF + s], (e / Lay::NKV) & 1, abort_flag, to);
+        uint32_t e[2] = {0, 0};
+        // masked scores are replaced, so key tiles are passed on as they are
+        auto pass = [&](int x, bool value, int b, int row, int limit) -> bool {
+          const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
+          const bool ok = mbar_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
           if (!__all_sync(0xffffffffu, ok)) return false;
-          if (zero) {
+          if (value) {
             uint32_t w[4];
             block_words(limit - row, args.mask.keys == nullptr ? nullptr : args.mask.keys + b * args.mask.stride + row,
                         lane, w);
-            zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
+            zero_rows<D>(sbase + (ring.tile0 + s) * Lay::TILE, w, lane);
             __syncwarp();
           }
           if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);
+          x ? ++e[1] : ++e[0];
           return true;
         };
-        walk(
-            [&](const CrossItem& it, const CrossRange& r0, const CrossRange& r1) {
-              b = it.b;
-              k0[0] = r0.k0;
-              k0[1] = r1.k0;
-              lim[0] = r0.limit;
-              lim[1] = r1.limit;
-            },
-            [&](int x, uint32_t e, uint32_t f) -> bool {
-              return !(f & CW_NEW) || fix(e, pb[x], prow[x], plim[x], true);
-            },
-            [&](int x, uint32_t e, uint32_t f, int k) -> bool {
-              pb[x] = b;
-              prow[x] = (k0[x] + k) * 128;
-              plim[x] = lim[x];
-              return !(f & CW_NEW) || fix(e, b, prow[x], plim[x], false);
-            });
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+          const int len = len_of(it.b);
+          const CrossRange r = cross_range(plan, len, it.sp[0]);
+          for (int k = 0; ok && k <= r.nk; ++k)
+            for (int x = 0; ok && x < ring.count; ++x) {
+              const int row = (r.k0 + x * r.nk + k) * 128;
+              if (k > 0) ok = pass(x, true, it.b, row - 128, len);
+              if (ok && k < r.nk) ok = pass(x, false, it.b, row, len);
+            }
+        }
       }
-    } else if (warp == 13) {
-      // ============================================================== MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
-        constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
-        constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
-        const uint64_t q0 = sdesc_sw128(sbase + Lay::Q_OFF, 16, 1024), k0 = sdesc_sw128(sbase + Lay::KV_OFF, 16, 1024),
-                       v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024);
-        uint32_t qn = 0;                  // query tiles taken
-        uint32_t qslot = 0;               // query slot of each job, 8 bits each
-        uint32_t par = 0, jpar = 0;       // bit x: parity of job slot x's P V products, of its jobs
-        uint32_t begun = 0;               // bit x: job slot x has begun a job
-        walk([](const CrossItem&, const CrossRange&, const CrossRange&) {},
-             [&](int x, uint32_t e, uint32_t f) -> bool {
-               const uint32_t s = e % Lay::NKV, p = (par >> x) & 1;
-               if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-               // the job's first product overwrites O: the epilogue has drained the last job's
-               if (f & CW_FIRST) {
-                 if (((begun >> x) & 1) && !mbar_wait(&bars[Lay::OE + x], ((jpar >> x) & 1) ^ 1, abort_flag, to))
-                   return false;
-                 begun |= 1u << x;
-                 jpar ^= 1u << x;
-               }
-               if (!mbar_wait(&bars[Lay::PF + x], p, abort_flag, to)) return false;
-               tc_fence_after();
-               const uint64_t va = v0 + s * (Lay::TILE >> 4);
-               const uint32_t o = tmem + 256 + D * x, a = tmem + 128 * x;
-               mma_ts(o, a, va, id_o, f & CW_FIRST ? 0u : 1u);
+    } else if (lane == 0) {
+      // ============================================================== MMA issuer of job x
+      const int x = warp == 13 ? 0 : 1;
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
+      constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
+      const uint64_t q0 = sdesc_sw128(sbase + x * Lay::TILE, 16, 1024),
+                     k0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, 16, 1024),
+                     v0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, kCrossBlk, 1024);
+      const uint32_t ts = tmem + 128 * x, tacc = tmem + 256 + D * x;
+      uint32_t e = 0;                    // key and value tiles of earlier blocks
+      uint32_t item = 0;                // items begun
+      uint32_t jobs = 0, blocks = 0;    // jobs and P V products of this issuer
+      uint32_t quse = 0;                // parity of the two query slots' uses
+      uint32_t ve = 0;                  // the pending block: its value tile, place and release
+      bool pending = false, pfirst = false, plast = false;
+      int i = blockIdx.x, k = 0, nk = 0;
+      // Tiles are released by both issuers, also by the one that has no job at an item (it passes
+      // over them, so that it sees every phase of their barriers); where one issuer alone reads
+      // them (one tile per item, or split keys), it releases them twice.
+      const bool alone = plan.tiles == 1 || plan.splits > 1;
+      if (x == 1 && plan.tiles == 1 && plan.splits == 1) i = plan.items;  // no jobs in this slot
+      for (;;) {
+        if (pending) {  // P V
+          const uint32_t s = ring.slot(x, ve), p = blocks & 1;
+          if (!mbar_wait(&bars[FULL + s], ring.use(ve) & 1, abort_flag, to)) break;
+          // the job's first product overwrites O: the epilogue has drained the last job's
+          if (pfirst) {
+            if (jobs > 0 && !mbar_wait(&bars[Lay::OE + x], (jobs - 1) & 1, abort_flag, to)) break;
+            ++jobs;
+          }
+          const uint64_t va = v0 + s * (Lay::TILE >> 4);
+          if (!mbar_wait(&bars[Lay::PF + x], p, abort_flag, to)) break;
+          tc_fence_after();
+          mma_ts(tacc, ts, va, id_o, pfirst ? 0u : 1u);
 #pragma unroll
-               for (int kk = 1; kk < 4; ++kk) mma_ts(o, a + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-               if (!mbar_wait(&bars[Lay::PF + 2 + x], p, abort_flag, to)) return false;
-               tc_fence_after();
+          for (int kk = 1; kk < 4; ++kk) mma_ts(tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+          if (!mbar_wait(&bars[Lay::PF + 2 + x], p, abort_flag, to)) break;
+          tc_fence_after();
 #pragma unroll
-               for (int kk = 4; kk < 8; ++kk) mma_ts(o, a + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-               if (f & CW_DONE) tc_commit(&bars[Lay::KVE + s]);
-               if (f & CW_LAST) tc_commit(&bars[Lay::OF + x]);
-               par ^= 1u << x;
-               return true;
-             },
-             [&](int x, uint32_t e, uint32_t f, int) -> bool {
-               const uint32_t s = e % Lay::NKV;
-               if (f & CW_FIRST) {
-                 const uint32_t z = qn % Lay::NQ;
-                 if (!mbar_wait(&bars[Lay::QF + z], (qn / Lay::NQ) & 1, abort_flag, to)) return false;
-                 qslot = x ? (qslot & 0xffu) | (z << 8) : (qslot & 0xff00u) | z;
-                 ++qn;
-               }
-               if (!mbar_wait(&bars[FULL + s], (e / Lay::NKV) & 1, abort_flag, to)) return false;
-               tc_fence_after();
-               // S overwrites the columns that this job's previous P V reads P from: the tensor
-               // core runs the products of one thread in issue order
-               const uint64_t qa = q0 + ((qslot >> (8 * x)) & 255u) * (Lay::TILE >> 4), ka = k0 + s * (Lay::TILE >> 4);
+          for (int kk = 4; kk < 8; ++kk) mma_ts(tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+          tc_commit(&bars[Lay::KVE + s]);
+          if (alone) tc_commit(&bars[Lay::KVE + s]);
+          if (plast) tc_commit(&bars[Lay::OF + x]);
+          ++blocks;
+          pending = false;
+        }
+        // the next block of this job slot: moves on to the next item that has one
+        bool ok = true;
+        while (ok && k >= nk && i < plan.items) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+          nk = cross_range(plan, len_of(it.b), it.sp[0]).nk;
+          k = 0;
+          if (x == 1 && it.qt[1] < 0) {
+            for (const uint32_t end = e + 2 * nk; ok && e != end; ++e) {
+              const uint32_t s = ring.slot(x, e);
+              ok = mbar_wait(&bars[FULL + s], ring.use(e) & 1, abort_flag, to);
+              if (ok) mbar_arrive(&bars[Lay::KVE + s]);
+            }
+            nk = 0;
+          }
+          i += gridDim.x;
+          ++item;
+        }
+        if (!ok || k >= nk) break;
+        // S overwrites the columns that the P V above reads P from: the tensor core runs the
+        // products of one thread in issue order
+        const uint32_t slot = (item - 1) & 1, s = ring.slot(x, e);
+        if (k == 0) {
+          if (!mbar_wait(&bars[Lay::QF + 2 * slot + x], (quse >> slot) & 1, abort_flag, to)) break;
+          quse ^= 1u << slot;
+        }
+        if (!mbar_wait(&bars[FULL + s], ring.use(e) & 1, abort_flag, to)) break;
+        tc_fence_after();
+        const uint64_t qa = q0 + slot * (2 * Lay::TILE >> 4), ka = k0 + s * (Lay::TILE >> 4);
 #pragma unroll
-               for (int kk = 0; kk < D / 16; ++kk) {
-                 const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
-                 mma_ss(tmem + 128 * x, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
-               }
-               tc_commit(&bars[Lay::SF + x]);
-               if (f & CW_DONE) tc_commit(&bars[Lay::KVE + s]);
-               return true;
-             });
-        tc_commit(&bars[Lay::DRAIN]);
-        mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+          mma_ss(ts, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars[Lay::SF + x]);
+        tc_commit(&bars[Lay::KVE + s]);
+        if (alone) tc_commit(&bars[Lay::KVE + s]);
+        ve = e + 1;
+        e += 2;
+        pending = true;
+        pfirst = k == 0;
+        plast = k == nk - 1;
+        ++k;
       }
+      tc_commit(&bars[Lay::DRAIN + x]);
+      mbar_wait_drain(&bars[Lay::DRAIN + x], 0, to);
     }
   } else if (warp >= 8) {
     // ================================================================ epilogue
     const int row = threadIdx.x & 127;
-    uint32_t q = 0, jobs[2] = {0, 0};
+    uint32_t jobs = 0;              // jobs of each slot so far (a byte each, mod 256)
+    uint32_t qused = 0, qpar = 0;   // per query slot: ever loaded, parity of its loads
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
     };
-    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+    // the query tile of job x of item i into slot s, where there is such a job
+    auto load_q = [&](long long i, int x, uint32_t s) {
+      if (i >= plan.items) return;
+      const CrossItem it = cross_item(plan, args.heads, int(i));
+      const int qt = x ? it.qt[1] : it.qt[0];
+      if (qt < 0) return;
+      mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
+#pragma unroll
+      for (int c = 0; c < DH; ++c)
+        tma_load_4d(sbase + s * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + s], c * 64, qt * 128,
+                    it.h * args.q_h, it.b * args.q_b);
+      qused |= 1u << s;
+      qpar ^= 1u << s;
+    };
+    if (threadIdx.x == 256) {
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) load_q((long long)blockIdx.x + (s >> 1) * (long long)gridDim.x, s & 1, s);
+    }
+    __syncwarp();
+    uint32_t item = 0;
+#pragma unroll 1
+    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
       const CrossItem it = cross_item(plan, args.heads, i);
 #pragma unroll 1
       for (int x = 0; ok && x < 2; ++x) {
-        if (it.qt[x] < 0) continue;
-        const uint32_t par = jobs[x] & 1, s = q % Lay::NQ;
+        const uint32_t s = 2 * (item & 1) + x;
+        const int qt = x ? it.qt[1] : it.qt[0];
+        if (qt < 0) {
+          if (threadIdx.x == 256) load_q(i + 2ll * gridDim.x, x, s);
+          __syncwarp();
+          continue;
+        }
+        const uint32_t job = (jobs >> (8 * x)) & 255u;
+        jobs = x ? (jobs & 0xffu) | ((job + 1) & 255u) << 8 : (jobs & 0xff00u) | ((job + 1) & 255u);
         // two barriers in turn: the softmax may finish the next job before this wait begins
-        if (!(ok = wwait(&bars[Lay::LF + 2 * x + par], (jobs[x] >> 1) & 1))) break;
-        ++q;
-        ++jobs[x];
-        const float inv = inv_sum[(2 * x + par) * 128 + row];
-        if (!(ok = wwait(&bars[Lay::OF + x], par))) break;
+        if (!(ok = wwait(&bars[Lay::LF + 2 * x + (job & 1)], (job >> 1) & 1))) break;
+        const uint32_t tile = sbase + s * Lay::TILE;
+        float m2, l;  // maximum (base 2) and sum of the row
+        ld_shared_f2(tile + (row >> 5) * 4096 + lane * 8, m2, l);
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
+        const int tok = qt * 128 + row;
+        if (tok < args.n) {
+          const float l2 = l == 0.f ? -INFINITY : m2 + log2f(l);
+          const long long r = ((long long)it.b * args.heads + it.h) * args.n + tok;
+          if (plan.splits > 1)
+            args.part_lse[(long long)(it.sp[0] + x) * args.B * args.heads * args.n + r] = l2;
+          else if (args.lse != nullptr)
+            args.lse[r] = l2 * 0.69314718055994530942f;
+        }
+        __syncwarp();  // the statistics are read before the rows of this warp are staged over them
+        if (!(ok = wwait(&bars[Lay::OF + x], job & 1))) break;
         tc_fence_after();
         const uint32_t t = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
-        const int tok = it.qt[x] * 128 + row;
         if (plan.splits > 1) {
-          const long long r = (((long long)it.sp[x] * args.B + it.b) * args.heads + it.h) * args.n + tok;
+          const long long r = (((long long)(it.sp[0] + x) * args.B + it.b) * args.heads + it.h) * args.n + tok;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t v[32];
+            __syncwarp();  // lanes part below: TMEM is read by whole warps
             tmem_ld32(t + c, v);
             if (tok < args.n) {
 #pragma unroll
@@ -395,12 +377,19 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[Lay::OE + x]);
-          // the Q tile is free once its products are done, which this warp has waited for
-          if (threadIdx.x == 256) mbar_arrive(&bars[Lay::QE + s]);
+          if (lane == 0) {
+            mbar_arrive(&bars[Lay::ST + x]);
+            mbar_arrive(&bars[Lay::OE + x]);
+          }
+          // the statistics of every warp's rows are read before the next query tile comes
+          if (threadIdx.x == 256) {
+            ok = mbar_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
+            if (ok) load_q(i + 2ll * gridDim.x, x, s);
+          }
+          ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
           continue;
         }
-        const uint32_t stage = sbase + Lay::Q_OFF + s * Lay::TILE + row * 128;
+        const uint32_t stage = tile + row * 128;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t v[32];
@@ -421,23 +410,27 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         tc_fence_before();
         fence_async_smem();
         __syncwarp();
+        // ST before OE: the next job of this slot, and so the next arrivals at its ST, wait for OE,
+        // so no warp can arrive for it while another has yet to arrive for this job
         if (lane == 0) {
+          mbar_arrive(&bars[Lay::ST + x]);
           mbar_arrive(&bars[Lay::OE + x]);
-          mbar_arrive(&bars[Lay::ST]);
         }
         if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = mbar_wait(&bars[Lay::ST], (q - 1) & 1, abort_flag, to);
+          ok = mbar_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
 #pragma unroll
           for (int c = 0; ok && c < DH; ++c)
-            tma_store_4d(&maps.o, sbase + Lay::Q_OFF + s * Lay::TILE + c * kCrossBlk, c * 64, it.qt[x] * 128,
-                         it.h * args.o_h, it.b * args.o_b);
+            tma_store_4d(&maps.o, tile + c * kCrossBlk, c * 64, qt * 128, it.h * args.o_h, it.b * args.o_b);
           bulk_commit();
           bulk_wait_read();
-          mbar_arrive(&bars[Lay::QE + s]);
+          if (ok) load_q(i + 2ll * gridDim.x, x, s);
         }
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
       }
     }
+    if (threadIdx.x == 256)
+      for (int s = 0; s < 4; ++s)
+        if ((qused >> s) & 1u) mbar_wait_drain(&bars[Lay::QF + s], ((qpar >> s) & 1u) ^ 1u, to);
   } else {
     // ================================================================ softmax
     const int x = warp >> 2, row = threadIdx.x & 127;
@@ -450,12 +443,12 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
     };
-    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+    uint32_t item = 0;
+    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
       const CrossItem it = cross_item(plan, args.heads, i);
       const int qt = x ? it.qt[1] : it.qt[0];
       if (qt < 0) continue;
       const CrossRange r = cross_range(plan, len_of(it.b), x ? it.sp[1] : it.sp[0]);
-      const int tok = qt * 128 + row;
       // a warp whose rows all lie past the last query has nothing to compute
       const bool idle = qt * 128 + (warp & 3) * 32 >= args.n;
       const unsigned char* keys =
@@ -556,25 +549,19 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         m_run = m_use;
       }
       if (!ok) break;
-      const float inv = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : l_run;  // NaN stays NaN
-      inv_sum[(2 * x + (jobs & 1)) * 128 + row] = inv;
+      // the row's statistics for the epilogue, in the query tile that no product reads any more
+      st_shared_f2(sbase + (2 * (item & 1) + x) * Lay::TILE + (row >> 5) * 4096 + lane * 8, m_run * c2, l_run);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[Lay::LF + 2 * x + (jobs & 1)]);
       ++jobs;
-      if (tok < args.n) {
-        const float l2 = l_run == 0.f ? -INFINITY : m_run * c2 + log2f(l_run);
-        const long long rr = ((long long)it.b * args.heads + it.h) * args.n + tok;
-        if (plan.splits > 1)
-          args.part_lse[(long long)(x ? it.sp[1] : it.sp[0]) * args.B * args.heads * args.n + rr] = l2;
-        else if (args.lse != nullptr)
-          args.lse[rr] = l2 * 0.69314718055994530942f;
-      }
     }
   }
 
+  __syncwarp();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0 && args.err != nullptr) atomicCAS(args.err, 0, 1);
-  if (warp == 13) {
+  if (warp == 14) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

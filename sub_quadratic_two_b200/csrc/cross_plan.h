@@ -18,7 +18,7 @@ struct CrossPlan {
   int qtiles;       // 128-row query tiles per (batch, head)
   int kblocks;      // 128-key blocks of m
   int tiles;        // query tiles per item: 2 (sharing keys) or 1
-  int splits;       // jobs that share the keys of a query tile (1: not split)
+  int splits;       // jobs that share the keys of a query tile: even, or 1 (not split)
   int per_bh;       // items per (batch, head)
   int items;        // items in all
   FastDiv f_per_bh, f_heads, f_group, f_sp;
@@ -43,18 +43,18 @@ inline CrossPlan make_cross_plan(int B, int heads, int kv_heads, int n, int m) {
     long long s = 2 * kCrossPlanSms / all;             // two jobs per SM
     const long long most = p.kblocks / 2;              // at least two blocks per job
     s = s < most ? s : most;
-    p.splits = int(s < 64 ? s : 64);
+    p.splits = int(s < 64 ? s : 64) & ~1;              // an item holds two of them
     if (p.splits < 2) p.splits = 1;
   }
   if (p.splits > 1)
-    p.per_bh = p.qtiles * ((p.splits + 1) / 2);
+    p.per_bh = p.qtiles * (p.splits / 2);
   else
     p.per_bh = (p.qtiles + p.tiles - 1) / p.tiles;
   p.items = B * heads * p.per_bh;
   p.f_per_bh = make_fastdiv(uint32_t(p.per_bh));
   p.f_heads = make_fastdiv(uint32_t(heads));
   p.f_group = make_fastdiv(uint32_t(heads / kv_heads));
-  p.f_sp = make_fastdiv(uint32_t((p.splits + 1) / 2));
+  p.f_sp = make_fastdiv(uint32_t(p.splits > 1 ? p.splits / 2 : 1));
   return p;
 }
 
@@ -65,9 +65,8 @@ SQ_HD CrossItem cross_item(const CrossPlan& p, int heads, int i) {
   it.h = bh - it.b * heads;
   it.hk = fdiv(it.h, p.f_group);
   if (p.splits > 1) {
-    const int qt = fdiv(r, p.f_sp), s = 2 * (r - qt * ((p.splits + 1) / 2));
-    it.qt[0] = qt;
-    it.qt[1] = s + 1 < p.splits ? qt : -1;
+    const int qt = fdiv(r, p.f_sp), s = 2 * (r - qt * (p.splits / 2));
+    it.qt[0] = it.qt[1] = qt;
     it.sp[0] = s;
     it.sp[1] = s + 1;
     it.shared = false;
@@ -81,18 +80,19 @@ SQ_HD CrossItem cross_item(const CrossPlan& p, int heads, int i) {
 }
 
 // Key blocks [k0, k0 + nk) of a job and the bound its keys lie below, for `len` keys that may
-// count. nk is at least 1: a job without keys runs one block whose keys are all masked.
+// count. nk is the same for every job of a batch row and at least 1: a job short of keys runs
+// blocks whose keys are all masked.
 struct CrossRange {
   int k0, nk, limit;
 };
 SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   const int nb = (len + 127) >> 7;
-  const int per = p.splits > 1 ? (nb + p.splits - 1) / p.splits : nb;
   CrossRange r;
-  r.k0 = sp * per;
-  const int k1 = r.k0 + per < nb ? r.k0 + per : nb;
-  r.nk = k1 - r.k0 > 1 ? k1 - r.k0 : 1;
-  r.limit = k1 * 128 < len ? k1 * 128 : len;
+  r.nk = p.splits > 1 ? (nb + p.splits - 1) / p.splits : nb;
+  if (r.nk < 1) r.nk = 1;
+  r.k0 = sp * r.nk;
+  const int end = (r.k0 + r.nk) * 128;
+  r.limit = end < len ? end : len;
   return r;
 }
 

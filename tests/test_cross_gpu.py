@@ -61,6 +61,25 @@ def test_bf16_shapes(cuda_ok, B, h, hk, n, m, d, layout):
 
 
 @pytest.mark.parametrize("B,h,hk,n,m,d", [
+    (1, 24, 24, 1, 6000, 128), (1, 3, 3, 1, 27280, 128), (2, 5, 5, 3, 9000, 64), (1, 2, 1, 129, 8200, 128),
+    (1, 37, 37, 128, 5000, 64)])
+def test_few_queries_over_long_states(cuda_ok, B, h, hk, n, m, d):
+    # the keys of a query tile are split over jobs of many blocks each
+    q, k, v, do = problem(m + h, B, h, hk, n, m, d)
+    for _ in range(3):
+        check(q, k, v, do, backward_too=False)
+
+
+@pytest.mark.parametrize("dtype,h,n,m,d", [(BF16, 40, 1100, 520, 64), (BF16, 100, 300, 300, 128), (BF16, 330, 100, 130, 64)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_many_items_with_odd_tiles(cuda_ok, dtype, h, n, m, d, padded):
+    # query tiles taken in pairs, the last of a head alone, several items per SM
+    q, k, v, do = problem(h, 2, h, h, n, m, d)
+    lens = torch.tensor([m, m // 3], dtype=torch.int32, device="cuda") if padded else None
+    check(q, k, v, do, kv_lens=lens)
+
+
+@pytest.mark.parametrize("B,h,hk,n,m,d", [
     (1, 1, 1, 1, 1, 32), (1, 2, 2, 3, 2, 64), (2, 2, 1, 63, 65, 96), (1, 2, 2, 64, 64, 128), (1, 2, 2, 65, 63, 160),
     (1, 4, 2, 130, 77, 192), (1, 1, 1, 33, 300, 224), (2, 2, 2, 100, 130, 256), (1, 3, 3, 257, 129, 32),
     (1, 2, 2, 1, 2000, 64), (1, 2, 1, 700, 1, 128),
