@@ -12,15 +12,15 @@
 //                   first thread then loads the job's query tile of the item after next there
 //   warp 12         TMA loads of key and value tiles, K(0) V(0) K(1) V(1) ... in a ring (a ring for
 //                   each job where the keys are split)
-//   warps 13, 15    one thread each issues the tcgen05.mma of job 0, job 1: what a thread spends
-//                   between its products (waits, addresses: some 100 cycles each) passes under
-//                   the products of the other
+//   warp 13         issues every tcgen05.mma (the whole warp runs the loop, one lane's count)
 //   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies
 //                   there may be NaN or infinite, and P = 0 times NaN is NaN)
 // TMEM (512 columns): S of job x at [128x, 128x+128), O at [256 + D x, ...). P overwrites S in
 // place as packed bf16 and goes to the tensor core in two halves of 64 keys.
-// Each job's products run S(0) | PV(0) S(1) | PV(1) S(2) | ...; while the tensor core works on
-// one job, the other job's softmax runs.
+// The order of the products is S0(0) S1(0) | PV0(0) S0(1) | PV1(0) S1(1) | ...: the jobs take
+// turns, and while the tensor core works on one, the other's softmax runs. (An issuing thread
+// per job let the two fall in step, products against products and softmax against softmax:
+// 232 us against 196 us at 27,280 x 512.)
 // A block of 128 x 128 costs the tensor core 4 x 128 x 128 x D flops (1,024 cycles at D = 128)
 // and the multi-function unit 128 x 128 exponentials (1,024 cycles at 16 a cycle): both are
 // near their limit at once.
@@ -29,12 +29,16 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 #include "cross_plan.h"
 #include "cross_tc.cuh"
 
 namespace sq {
 
 constexpr int kCrossThreads = 512;
+// Registers per thread: the eight softmax warps hold a whole row of scores (128), the others
+// need few. 256 * 184 + 256 * 72 = 512 * 128, the block's share at launch.
+constexpr int kCrossSoftmaxRegs = 184, kCrossOtherRegs = 72;
 struct alignas(64) CrossMaps {
   CUtensorMap q, k, v, o;
 };
@@ -58,13 +62,12 @@ struct CrossFwdLayout {
   static constexpr int NQ = 4;  // query tile of job x of the CTA's j-th item: slot 2 (j & 1) + x
   static constexpr int NKV = D == 128 ? 3 : 8;  // ring of key and value tiles, behind the query tiles
   // Split keys: a CTA has one item, so query slots 2 and 3 are free, and each job takes half of
-  // the tiles behind slot 1 as a ring of its own. (With one ring for both, an issuer would not
-  // see the phases of the tiles that the other job reads, and a wait by parity needs every phase.)
+  // the tiles behind slot 1 as a ring of its own.
   static constexpr int NS = (NKV + 2) / 2;
   static constexpr int NB = NKV > 2 * NS ? NKV : 2 * NS;  // ring barriers of each kind
   static constexpr int BAR_OFF = (NQ + NKV) * TILE;
   static constexpr int QF = 0, KVF = QF + NQ, KVE = KVF + NB, RDY = KVE + NB, SF = RDY + NB, PF = SF + 2, OF = PF + 4,
-                       OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 2, NBAR = DRAIN + 2;
+                       OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 2, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -79,7 +82,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
   const CrossPlan& plan = args.plan;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint64_t to = args.timeout_ns;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts aligned
     if (threadIdx.x == 0) atomicCAS(args.err, 0, 1);
@@ -88,10 +91,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::NBAR; ++i) {
-      // key and value tiles are released by both issuers (or twice by the only one that reads
-      // them); the softmax and epilogue warps arrive one by one
-      const int count = i >= Lay::KVE && i < Lay::RDY ? 2
-                        : (i >= Lay::PF && i < Lay::OF) || (i >= Lay::OE && i < Lay::DRAIN) ? 4 : 1;
+      // the softmax and epilogue warps arrive one by one
+      const int count = (i >= Lay::PF && i < Lay::OF) || (i >= Lay::OE && i < Lay::DRAIN) ? 4 : 1;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -136,13 +137,14 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     return len_v;
   };
   if (warp >= 12) {
+    regs_give<kCrossOtherRegs>();
     if (warp == 12) {
       // ============================================================== key and value loads
       if (lane == 0) {
         uint32_t e[2] = {0, 0};
         auto load = [&](int x, const CUtensorMap* m, int row, int h, int b) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
-          if (!mbar_wait(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
+          if (!mbar_wait_inline(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
           mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         // masked scores are replaced, so key tiles are passed on as they are
         auto pass = [&](int x, bool value, int b, int row, int limit) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
-          const bool ok = mbar_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
+          const bool ok = mbar_wait_inline(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
           if (!__all_sync(0xffffffffu, ok)) return false;
           if (value) {
             uint32_t w[4];
@@ -203,107 +205,117 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             }
         }
       }
-    } else if (lane == 0) {
-      // ============================================================== MMA issuer of job x
-      const int x = warp == 13 ? 0 : 1;
+    } else if (warp == 13) {
+      // ============================================================== MMA issuer
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
       constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
-      const uint64_t q0 = sdesc_sw128(sbase + x * Lay::TILE, 16, 1024),
-                     k0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, 16, 1024),
+      const uint32_t el = elect_one(), tm = uniform(tmem);
+      const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, 16, 1024),
                      v0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, kCrossBlk, 1024);
-      const uint32_t ts = tmem + 128 * x, tacc = tmem + 256 + D * x;
-      uint32_t e = 0;                    // key and value tiles of earlier blocks
-      uint32_t item = 0;                // items begun
-      uint32_t jobs = 0, blocks = 0;    // jobs and P V products of this issuer
-      uint32_t quse = 0;                // parity of the two query slots' uses
-      uint32_t ve = 0;                  // the pending block: its value tile, place and release
-      bool pending = false, pfirst = false, plast = false;
-      int i = blockIdx.x, k = 0, nk = 0;
-      // Tiles are released by both issuers, also by the one that has no job at an item (it passes
-      // over them, so that it sees every phase of their barriers); where one issuer alone reads
-      // them (one tile per item, or split keys), it releases them twice.
-      const bool alone = plan.tiles == 1 || plan.splits > 1;
-      if (x == 1 && plan.tiles == 1 && plan.splits == 1) i = plan.items;  // no jobs in this slot
-      for (;;) {
-        if (pending) {  // P V
-          const uint32_t s = ring.slot(x, ve), p = blocks & 1;
-          if (!mbar_wait(&bars[FULL + s], ring.use(ve) & 1, abort_flag, to)) break;
-          // the job's first product overwrites O: the epilogue has drained the last job's
-          if (pfirst) {
-            if (jobs > 0 && !mbar_wait(&bars[Lay::OE + x], (jobs - 1) & 1, abort_flag, to)) break;
-            ++jobs;
-          }
+      auto wait = [&](int bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_inline(&bars[bar], parity, abort_flag, to)) != 0;
+      };
+      const bool own = ring.count == 2;
+      // ring places as slot | phase << 8, so that no step divides
+      uint32_t pos[2] = {0, ring.size};
+      auto next = [&](int r) -> uint32_t {
+        const uint32_t at = pos[r], first = r ? ring.size : 0u;
+        pos[r] = (at & 255u) + 1 == first + ring.size ? first | ((at & 256u) ^ 256u) : at + 1;
+        return at;
+      };
+      // job x: its pending block (scores issued, P V still to come), that block's value tile and
+      // place in the job; parity of its P V products; jobs begun; parities of its query slots
+      bool pend[2] = {false, false}, pfirst[2], plast[2], pnew[2], pdone[2];
+      uint32_t vpos[2] = {0, 0}, ppar[2] = {0, 0}, jobs[2] = {0, 0}, quse[2] = {0, 0};
+      uint32_t kpos = 0, slot = 0;
+      bool ok = true;
+      auto step = [&](auto X, bool scores, bool first, bool last, bool two) -> bool {
+        constexpr int x = decltype(X)::value;
+        const uint32_t ts = tm + 128 * x, tacc = tm + 256 + D * x;
+        if (pend[x]) {  // P V of the block before
+          const uint32_t s = vpos[x] & 255u;
           const uint64_t va = v0 + s * (Lay::TILE >> 4);
-          if (!mbar_wait(&bars[Lay::PF + x], p, abort_flag, to)) break;
-          tc_fence_after();
-          mma_ts(tacc, ts, va, id_o, pfirst ? 0u : 1u);
-#pragma unroll
-          for (int kk = 1; kk < 4; ++kk) mma_ts(tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-          if (!mbar_wait(&bars[Lay::PF + 2 + x], p, abort_flag, to)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk) mma_ts(tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-          tc_commit(&bars[Lay::KVE + s]);
-          if (alone) tc_commit(&bars[Lay::KVE + s]);
-          if (plast) tc_commit(&bars[Lay::OF + x]);
-          ++blocks;
-          pending = false;
-        }
-        // the next block of this job slot: moves on to the next item that has one
-        bool ok = true;
-        while (ok && k >= nk && i < plan.items) {
-          const CrossItem it = cross_item(plan, args.heads, i);
-          nk = cross_range(plan, len_of(it.b), it.sp[0]).nk;
-          k = 0;
-          if (x == 1 && it.qt[1] < 0) {
-            for (const uint32_t end = e + 2 * nk; ok && e != end; ++e) {
-              const uint32_t s = ring.slot(x, e);
-              ok = mbar_wait(&bars[FULL + s], ring.use(e) & 1, abort_flag, to);
-              if (ok) mbar_arrive(&bars[Lay::KVE + s]);
-            }
-            nk = 0;
+          if (pnew[x] && !wait(FULL + s, vpos[x] >> 8)) return false;
+          // the job's first product overwrites O: the epilogue has drained the last job's
+          if (pfirst[x]) {
+            if (jobs[x] > 0 && !wait(Lay::OE + x, (jobs[x] - 1) & 1)) return false;
+            ++jobs[x];
           }
-          i += gridDim.x;
-          ++item;
+          if (!wait(Lay::PF + x, ppar[x])) return false;
+          tc_fence_after();
+          mma_ts_by(el, tacc, ts, va, id_o, pfirst[x] ? 0u : 1u);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) mma_ts_by(el, tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+          if (!wait(Lay::PF + 2 + x, ppar[x])) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) mma_ts_by(el, tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+          if (pdone[x]) tc_commit_by(el, &bars[Lay::KVE + s]);
+          if (plast[x]) tc_commit_by(el, &bars[Lay::OF + x]);
+          ppar[x] ^= 1u;
+          pend[x] = false;
         }
-        if (!ok || k >= nk) break;
+        if (!scores) return true;
         // S overwrites the columns that the P V above reads P from: the tensor core runs the
         // products of one thread in issue order
-        const uint32_t slot = (item - 1) & 1, s = ring.slot(x, e);
-        if (k == 0) {
-          if (!mbar_wait(&bars[Lay::QF + 2 * slot + x], (quse >> slot) & 1, abort_flag, to)) break;
-          quse ^= 1u << slot;
+        const bool fresh = own || x == 0, done = own || x == 1 || !two;
+        if (fresh) {
+          kpos = next(own ? x : 0);
+          vpos[x] = next(own ? x : 0);
+          if (!wait(FULL + (kpos & 255u), kpos >> 8)) return false;
+        } else {
+          vpos[x] = vpos[0];
         }
-        if (!mbar_wait(&bars[FULL + s], ring.use(e) & 1, abort_flag, to)) break;
+        if (first) {
+          if (!wait(Lay::QF + slot + x, (quse[x] >> (slot >> 1)) & 1)) return false;
+          quse[x] ^= 1u << (slot >> 1);
+        }
         tc_fence_after();
-        const uint64_t qa = q0 + slot * (2 * Lay::TILE >> 4), ka = k0 + s * (Lay::TILE >> 4);
+        const uint64_t qa = q0 + (slot + x) * (Lay::TILE >> 4), ka = k0 + (kpos & 255u) * (Lay::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
-          mma_ss(ts, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
+          mma_ss_by(el, ts, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(&bars[Lay::SF + x]);
-        tc_commit(&bars[Lay::KVE + s]);
-        if (alone) tc_commit(&bars[Lay::KVE + s]);
-        ve = e + 1;
-        e += 2;
-        pending = true;
-        pfirst = k == 0;
-        plast = k == nk - 1;
-        ++k;
+        tc_commit_by(el, &bars[Lay::SF + x]);
+        if (done) tc_commit_by(el, &bars[Lay::KVE + (kpos & 255u)]);
+        pend[x] = true;
+        pfirst[x] = first;
+        plast[x] = last;
+        pnew[x] = fresh;
+        pdone[x] = done;
+        return true;
+      };
+#pragma unroll 1
+      for (int i = blockIdx.x; ok; i += gridDim.x, slot ^= 2u) {
+        // past the last item: one turn for the products still pending
+        const bool more = i < plan.items;
+        int nk = 1;
+        bool two = false;
+        if (more) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+          nk = cross_range(plan, int(uniform(uint32_t(len_of(it.b)))), it.sp[0]).nk;
+          two = it.qt[1] >= 0;
+        }
+#pragma unroll 1
+        for (int k = 0; ok && k < nk; ++k)
+          ok = step(std::integral_constant<int, 0>{}, more, k == 0, k == nk - 1, two) &&
+               step(std::integral_constant<int, 1>{}, more && two, k == 0, k == nk - 1, two);
+        if (!more) break;
       }
-      tc_commit(&bars[Lay::DRAIN + x]);
-      mbar_wait_drain(&bars[Lay::DRAIN + x], 0, to);
+      tc_commit_by(el, &bars[Lay::DRAIN]);
+      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
     }
   } else if (warp >= 8) {
     // ================================================================ epilogue
+    regs_give<kCrossOtherRegs>();
     const int row = threadIdx.x & 127;
     uint32_t jobs = 0;              // jobs of each slot so far (a byte each, mod 256)
     uint32_t qused = 0, qpar = 0;   // per query slot: ever loaded, parity of its loads
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
     };
     // the query tile of job x of item i into slot s, where there is such a job
     auto load_q = [&](long long i, int x, uint32_t s) {
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           // the statistics of every warp's rows are read before the next query tile comes
           if (threadIdx.x == 256) {
-            ok = mbar_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
+            ok = mbar_wait_inline(&bars[Lay::ST + x], job & 1, abort_flag, to);
             if (ok) load_q(i + 2ll * gridDim.x, x, s);
           }
           ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           mbar_arrive(&bars[Lay::OE + x]);
         }
         if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = mbar_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
+          ok = mbar_wait_inline(&bars[Lay::ST + x], job & 1, abort_flag, to);
 #pragma unroll
           for (int c = 0; ok && c < DH; ++c)
             tma_store_4d(&maps.o, tile + c * kCrossBlk, c * 64, qt * 128, it.h * args.o_h, it.b * args.o_b);
@@ -433,6 +445,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         if ((qused >> s) & 1u) mbar_wait_drain(&bars[Lay::QF + s], ((qpar >> s) & 1u) ^ 1u, to);
   } else {
     // ================================================================ softmax
+    regs_take<kCrossSoftmaxRegs>();
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + 128 * x;
     const uint32_t tO = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     uint32_t sc = 0, jobs = 0;
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, to)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
     };
     uint32_t item = 0;
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
@@ -469,7 +482,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           continue;
         }
-        // a block that does not count whole: its masked scores become -inf where they lie
+        // a block that does not count whole: its masked scores become -inf where they lie (kept
+        // apart from the code below, which most blocks run alone)
         if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -484,20 +498,24 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           tmem_st_wait();
         }
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[64];
-          tmem_ld64(tS + 64 * c, v);
-          float a[8];
+        uint32_t v[4][32];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) a[j] = fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 8]));
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
 #pragma unroll
-          for (int e = 16; e < 64; e += 16)
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(v[c]);
+        float a[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = fmax3(a[j], __uint_as_float(v[e + j]), __uint_as_float(v[e + j + 8]));
-          mx = fmax3(fmax3(mx, a[0], a[1]), fmax3(a[2], a[3], a[4]), fmax3(a[5], a[6], a[7]));
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (c == 0)
+              a[j] = fmaxf(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 8]));
+            else
+              a[j] = fmax3(a[j], __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 8]));
+            a[j] = fmax3(a[j], __uint_as_float(v[c][j + 16]), __uint_as_float(v[c][j + 24]));
+          }
         }
+        const float mx = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
         // the first block sets the maximum; a later one moves it only when it grows by more
         // than 2^8 (then O and the sum are rescaled), else its probabilities may exceed 1
         float m_use = mx, alpha = 1.f;
@@ -521,28 +539,25 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         const float neg = m_use == -INFINITY ? 0.f : -m_use * c2;  // a row without keys: every exponent is -inf
         const uint64_t neg2 = f2(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
-        // P of 64 keys at a time, packed over columns [32 c, 32 c + 32), whose scores are done with
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          if ((c ? w[2] | w[3] : w[0] | w[1]) == 0u) {  // no key counts: no exponentials
-            tmem_st16_zero(tS + 32 * c);
-            tmem_st16_zero(tS + 32 * c + 16);
-          } else {
-            uint32_t v[64], p[32];
-            tmem_ld64(tS + 64 * c, v);
+        // P packed over the columns that the scores lay in, 32 keys at a time; the first 64 keys are
+        // handed over while the third chunk's exponentials run, so that their stores are not waited for
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const uint64_t z = ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg2);
-              const float p0 = ex2_approx(f2_lo(z)), p1 = ex2_approx(f2_hi(z));
-              sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], f2(p0, p1));
-              p[e >> 1] = pack_bf16x2(p0, p1);
-            }
-            tmem_st32(tS + 32 * c, p);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t z = ffma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), c2x2, neg2);
+            const float p0 = ex2_approx(f2_lo(z)), p1 = ex2_approx(f2_hi(z));
+            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], f2(p0, p1));
+            p[e >> 1] = pack_bf16x2(p0, p1);
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[Lay::PF + 2 * c + x]);
+          tmem_st16(tS + 16 * c, p);
+          if (c >= 2) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[Lay::PF + 2 * (c - 2) + x]);
+          }
         }
         const uint64_t s2 = fadd2(sum[0], sum[1]);
         l_run = l_run * alpha + (f2_lo(s2) + f2_hi(s2));
