@@ -43,10 +43,6 @@ struct CrossBwdArgs {
   uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t to) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, to)) != 0;
-}
-
 // ==================================================================== dQ
 //
 // Roles (512 threads):
@@ -88,7 +84,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
   float* d_smem = reinterpret_cast<float*>(smem + Lay::D_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint64_t to = args.timeout_ns;
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicCAS(args.err, 0, 1);
@@ -163,7 +159,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         const int nk = blocks_of(it.b);
         for (int k = 0; ok && k < nk; ++k) {
           const uint32_t s = e % Lay::NK;
-          if (!(ok = mbar_wait(&bars[Lay::KE + s], ((e / Lay::NK) & 1) ^ 1, abort_flag, to))) break;
+          if (!(ok = cross_wait(&bars[Lay::KE + s], ((e / Lay::NK) & 1) ^ 1, abort_flag, to))) break;
           load(sbase + Lay::K_OFF + s * Lay::TILE, &maps.k, &bars[Lay::KF + s], k * 128, it.hk * args.k_h, it.b * args.k_b);
           ++e;
         }
@@ -179,12 +175,12 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         const int nk = blocks_of(it.b);
         for (int k = 0; ok && k < nk; ++k) {
           const uint32_t s = e % Lay::NV;
-          if (!(ok = mbar_wait(&bars[Lay::VE + s], ((e / Lay::NV) & 1) ^ 1, abort_flag, to))) break;
+          if (!(ok = cross_wait(&bars[Lay::VE + s], ((e / Lay::NV) & 1) ^ 1, abort_flag, to))) break;
           load(sbase + Lay::V_OFF + s * Lay::TILE, &maps.v, &bars[Lay::VF + s], k * 128, it.hk * args.v_h, it.b * args.v_b);
           ++e;
           if (k == 0) {
             const uint32_t z = q % Lay::NDO;
-            if (!(ok = mbar_wait(&bars[Lay::DOE + z], ((q / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
+            if (!(ok = cross_wait(&bars[Lay::DOE + z], ((q / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
             load(sbase + Lay::DO_OFF + z * Lay::TILE, &maps.dout, &bars[Lay::DOF + z], it.qt * 128, it.h * args.do_h,
                  it.b * args.do_b);
             ++q;
@@ -206,11 +202,11 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
           block_words(len - k * 128,
                       args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + k * 128, lane, w);
           const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
-          if (!(ok = warp_wait(&bars[Lay::KF + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
+          if (!(ok = cross_warp_wait(&bars[Lay::KF + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
           zero_rows<D>(sbase + Lay::K_OFF + sk * Lay::TILE, w, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::KR + sk]);
-          if (!(ok = warp_wait(&bars[Lay::VF + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
+          if (!(ok = cross_warp_wait(&bars[Lay::VF + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
           zero_rows<D>(sbase + Lay::V_OFF + sv * Lay::TILE, w, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::VR + sv]);
@@ -218,70 +214,81 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       }
     }
   } else if (warp == 13) {
-    if (lane == 0) {  // ---------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);  // S, dP: both operands K-major
-      constexpr uint32_t id_q = idesc_bf16_f32(128, D, 0, 1);    // dQ: A (dS) from TMEM, B (K) MN-major
-      constexpr int KREADY = MASKED ? Lay::KR : Lay::KF, VREADY = MASKED ? Lay::VR : Lay::VF;
-      // dQ(t): wait for dS(t), multiply by the key tile, release it
-      auto dq = [&](uint32_t t, uint32_t job, bool first, bool last) -> bool {
-        if (first && job > 0 && !mbar_wait(&bars[Lay::OE], (job - 1) & 1, abort_flag, to)) return false;
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);  // S, dP: both operands K-major
+    constexpr uint32_t id_q = idesc_bf16_f32(128, D, 0, 1);    // dQ: A (dS) from TMEM, B (K) MN-major
+    constexpr int KREADY = MASKED ? Lay::KR : Lay::KF, VREADY = MASKED ? Lay::VR : Lay::VF;
+    const uint32_t el = elect_one(), tm = uniform(tmem);
+    const uint64_t q0 = sdesc_sw128(sbase + Lay::Q_OFF, 16, 1024), o0 = sdesc_sw128(sbase + Lay::DO_OFF, 16, 1024),
+                   k0 = sdesc_sw128(sbase + Lay::K_OFF, 16, 1024), v0 = sdesc_sw128(sbase + Lay::V_OFF, 16, 1024),
+                   kt0 = sdesc_sw128(sbase + Lay::K_OFF, kCrossBlk, 1024);
+    auto wait = [&](int bar, uint32_t parity) -> bool {
+      return cross_warp_wait(&bars[bar], parity, abort_flag, to);
+    };
+    // dQ(t) += dS(t) K; the tile's first block overwrites what the epilogue has drained
+    auto dq = [&](uint32_t t, uint32_t job, bool first, bool last) -> bool {
+      if (first && job > 0 && !wait(Lay::OE, (job - 1) & 1)) return false;
+      tc_fence_after();
+      const uint32_t s = t % Lay::NK, a = tm + 128 * (t & 1);
+      const uint64_t ka = kt0 + s * (Lay::TILE >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts_by(el, tm + 384, a + (kk >> 2) * 64 + (kk & 3) * 8, ka + kk * (2048 >> 4), id_q,
+                  kk == 0 ? (first ? 0u : 1u) : 1u);
+      tc_commit_by(el, &bars[Lay::KE + s]);
+      if (last) tc_commit_by(el, &bars[Lay::OF]);
+      return true;
+    };
+    uint32_t t = 0, job = 0;
+    bool ok = true, prev = false, prev_first = false, prev_last = false;
+#pragma unroll 1
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
+      const Item it = item_of(i);
+      const int nk = int(uniform(uint32_t(blocks_of(it.b))));
+      const uint32_t z = job % Lay::NDO;
+      const uint64_t qa = q0 + (job & 1) * (Lay::TILE >> 4), da = o0 + z * (Lay::TILE >> 4);
+#pragma unroll 1
+      for (int k = 0; k < nk; ++k, ++t) {
+        const bool first = k == 0, last = k == nk - 1;
+        const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
+        // S(t) into the columns that dQ(t - 2) read dS from (issued before, so behind it)
+        if (!(ok = wait(KREADY + sk, (t / Lay::NK) & 1))) break;
+        if (first && !(ok = wait(Lay::QF + (job & 1), (job >> 1) & 1))) break;
         tc_fence_after();
-        const uint32_t s = t % Lay::NK, ka = sbase + Lay::K_OFF + s * Lay::TILE, a = tmem + 128 * (t & 1);
+        const uint64_t ka = k0 + sk * (Lay::TILE >> 4), va = v0 + sv * (Lay::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 384, a + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(ka + kk * 2048, kCrossBlk, 1024), id_q,
-                 (!first || kk > 0) ? 1u : 0u);
-        tc_commit(&bars[Lay::KE + s]);
-        if (last) tc_commit(&bars[Lay::OF]);
-        return true;
-      };
-      uint32_t t = 0, job = 0;
-      bool ok = true, prev = false, prev_first = false, prev_last = false;
-      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
-        const Item it = item_of(i);
-        const int nk = blocks_of(it.b);
-        const uint32_t qa = sbase + Lay::Q_OFF + (job & 1) * Lay::TILE;
-        const uint32_t z = job % Lay::NDO, da = sbase + Lay::DO_OFF + z * Lay::TILE;
-        for (int k = 0; k < nk; ++k, ++t) {
-          const bool first = k == 0, last = k == nk - 1;
-          const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
-          // S(t) into the columns that dQ(t - 2) read dS from (issued before, so behind it)
-          if (!(ok = mbar_wait(&bars[KREADY + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
-          if (first && !(ok = mbar_wait(&bars[Lay::QF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
-          tc_fence_after();
-          const uint32_t ka = sbase + Lay::K_OFF + sk * Lay::TILE, va = sbase + Lay::V_OFF + sv * Lay::TILE;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-            mma_ss(tmem + 128 * (t & 1), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), id_s,
-                   kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&bars[Lay::SF + (t & 1)]);
-          // dS(t - 1) is written, so dP(t - 1) has been read
-          if (prev && !(ok = mbar_wait(&bars[Lay::DSF], (t - 1) & 1, abort_flag, to))) break;
-          // at a new tile dO has yet to arrive: dQ of the last block goes first
-          if (prev && first && !(ok = dq(t - 1, job - 1, prev_first, prev_last))) break;
-          if (!(ok = mbar_wait(&bars[VREADY + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
-          if (first && !(ok = mbar_wait(&bars[Lay::DOF + z], (job / Lay::NDO) & 1, abort_flag, to))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-            mma_ss(tmem + 256, sdesc_sw128(da + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&bars[Lay::DPF]);
-          tc_commit(&bars[Lay::VE + sv]);
-          if (last) tc_commit(&bars[Lay::DOE + z]);
-          if (prev && !first && !(ok = dq(t - 1, job, prev_first, prev_last))) break;
-          prev = true;
-          prev_first = first;
-          prev_last = last;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+          mma_ss_by(el, tm + 128 * (t & 1), qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
         }
+        tc_commit_by(el, &bars[Lay::SF + (t & 1)]);
+        // dS(t - 1) is written, so dP(t - 1) has been read. At a new tile dO has yet to arrive: dQ
+        // of the last block goes first. Else the value tile is waited for ahead of dS.
+        if (!first && !(ok = wait(VREADY + sv, (t / Lay::NV) & 1))) break;
+        if (prev && !(ok = wait(Lay::DSF, (t - 1) & 1))) break;
+        if (first) {
+          if (prev && !(ok = dq(t - 1, job - 1, prev_first, prev_last))) break;
+          if (!(ok = wait(VREADY + sv, (t / Lay::NV) & 1))) break;
+          if (!(ok = wait(Lay::DOF + z, (job / Lay::NDO) & 1))) break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+          mma_ss_by(el, tm + 256, da + off, va + off, id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit_by(el, &bars[Lay::DPF]);
+        tc_commit_by(el, &bars[Lay::VE + sv]);
+        if (last) tc_commit_by(el, &bars[Lay::DOE + z]);
+        if (!first && !(ok = dq(t - 1, job, prev_first, prev_last))) break;
+        prev = true;
+        prev_first = first;
+        prev_last = last;
       }
-      if (ok && prev && mbar_wait(&bars[Lay::DSF], (t - 1) & 1, abort_flag, to)) dq(t - 1, job - 1, prev_first, prev_last);
-      tc_commit(&bars[Lay::DRAIN]);
-      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
     }
+    if (ok && prev && wait(Lay::DSF, (t - 1) & 1)) dq(t - 1, job - 1, prev_first, prev_last);
+    tc_commit_by(el, &bars[Lay::DRAIN]);
+    mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ D, dQ
     const int ew = warp & 3, row = threadIdx.x & 127;
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     auto make_d = [&](int i) -> bool {
       const Item it = item_of(i);
       const uint32_t par = made & 1;
-      if (!warp_wait(&bars[Lay::DE + par], ((made >> 1) & 1) ^ 1, abort_flag, to)) return false;
+      if (!cross_warp_wait(&bars[Lay::DE + par], ((made >> 1) & 1) ^ 1, abort_flag, to)) return false;
       const long long base = ((long long)it.b * args.heads + it.h) * args.n;
       const int r0 = it.qt * 128 + ew * 32 + lane / LPR, c = (lane % LPR) * 8;
 #pragma unroll 1
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
       if (i + int(gridDim.x) < args.items && !(ok = make_d(i + gridDim.x))) break;
       const Item it = item_of(i);
-      if (!(ok = warp_wait(&bars[Lay::OF], job & 1, abort_flag, to))) break;
+      if (!(ok = cross_warp_wait(&bars[Lay::OF], job & 1, abort_flag, to))) break;
       tc_fence_after();
       const uint32_t t = tmem + (uint32_t(ew * 32) << 16) + 384;
       const uint32_t tile = sbase + Lay::Q_OFF + (job & 1) * Lay::TILE, stage = tile + row * 128;
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         mbar_arrive(&bars[Lay::OE]);
       }
       if (threadIdx.x == 256) {
-        ok = mbar_wait(&bars[Lay::ST], job & 1, abort_flag, to);
+        ok = cross_wait(&bars[Lay::ST], job & 1, abort_flag, to);
 #pragma unroll
         for (int c = 0; ok && c < DH; ++c)
           tma_store_4d(&maps.dq, tile + c * kCrossBlk, c * 64, it.qt * 128, it.h * args.dq_h, it.b * args.dq_b);
@@ -414,8 +421,22 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         if (len - k * 128 < 128 || keys != nullptr) block_words(len - k * 128, keys, lane, w);
         const uint32_t wa = g ? w[2] : w[0], wb = g ? w[3] : w[1];
         const uint32_t tS = tmem + lanes + 128 * (t & 1) + 64 * g, tP = tmem + lanes + 256 + 64 * g;
-        if (!(ok = warp_wait(&bars[Lay::SF + (t & 1)], (t >> 1) & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::SF + (t & 1)], (t >> 1) & 1, abort_flag, to))) break;
         tc_fence_after();
+        // a block that does not count whole: its masked scores become -inf where they lie
+        if ((wa & wb) != ~0u && !idle) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t word = c ? wb : wa;
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * c, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((word >> e) & 1u)) v[e] = 0xff800000u;
+            tmem_st32(tS + 32 * c, v);
+          }
+          tmem_st_wait();
+        }
         float p[64];
         if (!idle) {
           uint32_t v[2][16];
@@ -425,27 +446,21 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
             uint32_t(&u)[16] = v[c & 1];
             tmem_ld_wait(u);
             if (c < 3) tmem_ld16_async(tS + 16 * (c + 1), v[(c + 1) & 1]);
-            const uint32_t word = (c < 2 ? wa : wb) >> (16 * (c & 1)) & 0xffffu;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const uint64_t z = ffma2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), c2x2, neg2);
               p[16 * c + e] = ex2_approx(f2_lo(z));
               p[16 * c + e + 1] = ex2_approx(f2_hi(z));
             }
-            if (word != 0xffffu) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!((word >> e) & 1u)) p[16 * c + e] = 0.f;
-            }
           }
         }
         if (k == 0) {
-          if (!(ok = warp_wait(&bars[Lay::DF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
+          if (!(ok = cross_warp_wait(&bars[Lay::DF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
           Dv = d_smem[(job & 1) * 128 + row];
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::DE + (job & 1)]);
         }
-        if (!(ok = warp_wait(&bars[Lay::DPF], t & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::DPF], t & 1, abort_flag, to))) break;
         tc_fence_after();
         if (!idle) {
           const uint64_t nd = f2(-Dv, -Dv);
@@ -524,7 +539,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint64_t to = args.timeout_ns;
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicCAS(args.err, 0, 1);
@@ -603,12 +618,12 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         if (u.t0 >= u.t1) continue;
         for (int t = u.t0; ok && t < u.t1; ++t) {
           if (t == u.t0) {
-            if (!(ok = mbar_wait(&bars[Lay::KE], (units & 1) ^ 1, abort_flag, to))) break;
+            if (!(ok = cross_wait(&bars[Lay::KE], (units & 1) ^ 1, abort_flag, to))) break;
             load(sbase + Lay::K_OFF, &maps.k, &bars[Lay::KF], u.kb * 128, u.hk * args.k_h, u.b * args.k_b);
           }
           const int g = fdiv(t, args.f_qtiles), h = u.hk * args.group + g;
           const uint32_t s = e % Lay::NQ;
-          if (!(ok = mbar_wait(&bars[Lay::QE + s], ((e / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
+          if (!(ok = cross_wait(&bars[Lay::QE + s], ((e / Lay::NQ) & 1) ^ 1, abort_flag, to))) break;
           load(sbase + Lay::Q_OFF + s * Lay::TILE, &maps.q, &bars[Lay::QF + s], (t - g * args.qtiles) * 128,
                h * args.q_h, u.b * args.q_b);
           ++e;
@@ -627,12 +642,12 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         if (u.t0 >= u.t1) continue;
         for (int t = u.t0; ok && t < u.t1; ++t) {
           if (t == u.t0) {
-            if (!(ok = mbar_wait(&bars[Lay::VE], (units & 1) ^ 1, abort_flag, to))) break;
+            if (!(ok = cross_wait(&bars[Lay::VE], (units & 1) ^ 1, abort_flag, to))) break;
             load(sbase + Lay::V_OFF, &maps.v, &bars[Lay::VF], u.kb * 128, u.hk * args.v_h, u.b * args.v_b);
           }
           const int g = fdiv(t, args.f_qtiles), h = u.hk * args.group + g;
           const uint32_t s = e % Lay::NDO;
-          if (!(ok = mbar_wait(&bars[Lay::DOE + s], ((e / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
+          if (!(ok = cross_wait(&bars[Lay::DOE + s], ((e / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
           load(sbase + Lay::DO_OFF + s * Lay::TILE, &maps.dout, &bars[Lay::DOF + s], (t - g * args.qtiles) * 128,
                h * args.do_h, u.b * args.do_b);
           ++e;
@@ -664,7 +679,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
           }
         }
         const uint32_t s = t_all & 1;
-        if (!(ok = warp_wait(&bars[Lay::VECE + s], ((t_all >> 1) & 1) ^ 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::VECE + s], ((t_all >> 1) & 1) ^ 1, abort_flag, to))) break;
         float* vec = reinterpret_cast<float*>(smem + Lay::VEC_OFF) + s * 256;
         *reinterpret_cast<float4*>(vec + lane * 4) = make_float4(l[0], l[1], l[2], l[3]);
         *reinterpret_cast<float4*>(vec + 128 + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
@@ -673,90 +688,109 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       }
     }
   } else if (warp == 13) {
-    if (lane == 0) {  // ---------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t id_acc = idesc_bf16_f32(128, D, 0, 1);
-      const uint32_t ka = sbase + Lay::K_OFF, va = sbase + Lay::V_OFF;
-      bool ok = true;
-      // the (unit, tile) pairs in order, with one pair of look-ahead
-      struct Step {
-        int i, t, t0, t1;
-        uint32_t unit;
-        bool ok;
-      };
-      auto seek = [&](int i, uint32_t unit) -> Step {
-        for (; i < args.items; i += gridDim.x) {
-          const Unit u = unit_of(i);
-          if (u.t0 < u.t1) return Step{i, u.t0, u.t0, u.t1, unit, true};
-        }
-        return Step{i, 0, 0, 0, unit, false};
-      };
-      auto after = [&](const Step& s) -> Step {
-        if (s.t + 1 < s.t1) return Step{s.i, s.t + 1, s.t0, s.t1, s.unit, true};
-        return seek(s.i + gridDim.x, s.unit + 1);
-      };
-      auto s_mma = [&](const Step& s, uint32_t e) -> bool {
-        const uint32_t z = e % Lay::NQ, qa = sbase + Lay::Q_OFF + z * Lay::TILE;
-        if (s.t == s.t0 && !mbar_wait(&bars[Lay::KF], s.unit & 1, abort_flag, to)) return false;
-        if (!mbar_wait(&bars[Lay::QF + z], (e / Lay::NQ) & 1, abort_flag, to)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-          mma_ss(tmem, sdesc_sw128(ka + off, 16, 1024), sdesc_sw128(qa + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&bars[Lay::SF]);
-        if (s.t == s.t1 - 1) tc_commit(&bars[Lay::KE]);
-        return true;
-      };
-      auto dp_mma = [&](const Step& s, uint32_t e) -> bool {
-        const uint32_t z = e % Lay::NDO, da = sbase + Lay::DO_OFF + z * Lay::TILE;
-        if (s.t == s.t0 && !mbar_wait(&bars[Lay::VF], s.unit & 1, abort_flag, to)) return false;
-        if (!mbar_wait(&bars[Lay::DOF + z], (e / Lay::NDO) & 1, abort_flag, to)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kCrossBlk + (kk & 3) * 32;
-          mma_ss(tmem + 128, sdesc_sw128(va + off, 16, 1024), sdesc_sw128(da + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&bars[Lay::DPF]);
-        if (s.t == s.t1 - 1) tc_commit(&bars[Lay::VE]);
-        return true;
-      };
-      uint32_t e = 0;
-      Step cur = seek(blockIdx.x, 0);
-      if (cur.ok) ok = s_mma(cur, 0) && dp_mma(cur, 0);
-      while (ok && cur.ok) {
-        const Step nxt = after(cur);
-        const bool first = cur.t == cur.t0, last = cur.t == cur.t1 - 1;
-        // dV += P^T dO (the unit's first overwrites what the epilogue has drained)
-        if (!(ok = mbar_wait(&bars[Lay::PF], e & 1, abort_flag, to))) break;
-        if (first && cur.unit > 0 && !(ok = mbar_wait(&bars[Lay::ACCE], (cur.unit - 1) & 1, abort_flag, to))) break;
-        tc_fence_after();
-        const uint32_t zo = e % Lay::NDO, da = sbase + Lay::DO_OFF + zo * Lay::TILE;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(da + kk * 2048, kCrossBlk, 1024), id_acc,
-                 (!first || kk > 0) ? 1u : 0u);
-        tc_commit(&bars[Lay::DOE + zo]);
-        if (nxt.ok && !(ok = s_mma(nxt, e + 1))) break;
-        // dK += dS^T Q
-        if (!(ok = mbar_wait(&bars[Lay::DSF], e & 1, abort_flag, to))) break;
-        tc_fence_after();
-        const uint32_t zq = e % Lay::NQ, qa = sbase + Lay::Q_OFF + zq * Lay::TILE;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(qa + kk * 2048, kCrossBlk, 1024),
-                 id_acc, (!first || kk > 0) ? 1u : 0u);
-        tc_commit(&bars[Lay::QE + zq]);
-        if (last) tc_commit(&bars[Lay::ACCF]);
-        if (nxt.ok && !(ok = dp_mma(nxt, e + 1))) break;
-        cur = nxt;
-        ++e;
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t id_acc = idesc_bf16_f32(128, D, 0, 1);
+    const uint32_t el = elect_one(), tm = uniform(tmem);
+    const uint64_t ka = sdesc_sw128(sbase + Lay::K_OFF, 16, 1024), va = sdesc_sw128(sbase + Lay::V_OFF, 16, 1024),
+                   q0 = sdesc_sw128(sbase + Lay::Q_OFF, 16, 1024), o0 = sdesc_sw128(sbase + Lay::DO_OFF, 16, 1024),
+                   qt0 = sdesc_sw128(sbase + Lay::Q_OFF, kCrossBlk, 1024),
+                   ot0 = sdesc_sw128(sbase + Lay::DO_OFF, kCrossBlk, 1024);
+    auto wait = [&](int bar, uint32_t parity) -> bool {
+      return cross_warp_wait(&bars[bar], parity, abort_flag, to);
+    };
+    // the (unit, tile) pairs in order, with one pair of look-ahead
+    struct Step {
+      int i, t, t0, t1;
+      uint32_t unit;
+      bool ok;
+    };
+    auto seek = [&](int i, uint32_t unit) -> Step {
+#pragma unroll 1
+      for (; i < args.items; i += gridDim.x) {
+        const Unit u = unit_of(i);
+        const int t0 = int(uniform(uint32_t(u.t0))), t1 = int(uniform(uint32_t(u.t1)));
+        if (t0 < t1) return Step{i, t0, t0, t1, unit, true};
       }
-      tc_commit(&bars[Lay::DRAIN]);
-      mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
+      return Step{i, 0, 0, 0, unit, false};
+    };
+    // S(e) and dP(e), e: the tile's number over all units
+    auto s_mma = [&](const Step& s, uint32_t e) -> bool {
+      const uint32_t z = e % Lay::NQ;
+      if (s.t == s.t0 && !wait(Lay::KF, s.unit & 1)) return false;
+      if (!wait(Lay::QF + z, (e / Lay::NQ) & 1)) return false;
+      tc_fence_after();
+      const uint64_t qa = q0 + z * (Lay::TILE >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+        mma_ss_by(el, tm, ka + off, qa + off, id_s, kk > 0 ? 1u : 0u);
+      }
+      tc_commit_by(el, &bars[Lay::SF]);
+      if (s.t == s.t1 - 1) tc_commit_by(el, &bars[Lay::KE]);
+      return true;
+    };
+    auto dp_mma = [&](const Step& s, uint32_t e) -> bool {
+      const uint32_t z = e % Lay::NDO;
+      if (s.t == s.t0 && !wait(Lay::VF, s.unit & 1)) return false;
+      if (!wait(Lay::DOF + z, (e / Lay::NDO) & 1)) return false;
+      tc_fence_after();
+      const uint64_t da = o0 + z * (Lay::TILE >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
+        mma_ss_by(el, tm + 128, va + off, da + off, id_s, kk > 0 ? 1u : 0u);
+      }
+      tc_commit_by(el, &bars[Lay::DPF]);
+      if (s.t == s.t1 - 1) tc_commit_by(el, &bars[Lay::VE]);
+      return true;
+    };
+    uint32_t e = 0;
+    Step cur{}, nxt = seek(blockIdx.x, 0);
+    bool ok = true;
+    // e counts the tiles whose dV and dK are issued; the loop body issues those of tile `cur` (none
+    // in the first turn) between S and dP of tile `nxt`
+#pragma unroll 1
+    while (ok && (cur.ok || nxt.ok)) {
+      const bool first = cur.t == cur.t0, last = cur.t == cur.t1 - 1;
+      const uint32_t n = cur.ok ? e + 1 : 0;  // number of tile `nxt`
+      if (cur.ok) {  // dV += P^T dO (the unit's first overwrites what the epilogue has drained)
+        if (first && cur.unit > 0 && !(ok = wait(Lay::ACCE, (cur.unit - 1) & 1))) break;
+        if (!(ok = wait(Lay::PF, e & 1))) break;
+        tc_fence_after();
+        const uint32_t z = e % Lay::NDO;
+        const uint64_t da = ot0 + z * (Lay::TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_by(el, tm + 256, tm + (kk >> 2) * 64 + (kk & 3) * 8, da + kk * (2048 >> 4), id_acc,
+                    kk == 0 ? (first ? 0u : 1u) : 1u);
+        tc_commit_by(el, &bars[Lay::DOE + z]);
+      }
+      if (nxt.ok && !(ok = s_mma(nxt, n))) break;
+      if (cur.ok) {  // dK += dS^T Q
+        if (!(ok = wait(Lay::DSF, e & 1))) break;
+        tc_fence_after();
+        const uint32_t z = e % Lay::NQ;
+        const uint64_t qa = qt0 + z * (Lay::TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_by(el, tm + 384, tm + 128 + (kk >> 2) * 64 + (kk & 3) * 8, qa + kk * (2048 >> 4), id_acc,
+                    kk == 0 ? (first ? 0u : 1u) : 1u);
+        tc_commit_by(el, &bars[Lay::QE + z]);
+        if (last) tc_commit_by(el, &bars[Lay::ACCF]);
+      }
+      if (nxt.ok && !(ok = dp_mma(nxt, n))) break;
+      if (cur.ok) ++e;
+      cur = nxt;
+      if (cur.ok) {
+        if (cur.t + 1 < cur.t1)
+          nxt.t = cur.t + 1;
+        else
+          nxt = seek(cur.i + gridDim.x, cur.unit + 1);
+      }
     }
+    tc_commit_by(el, &bars[Lay::DRAIN]);
+    mbar_wait_drain(&bars[Lay::DRAIN], 0, to);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ dK, dV
     const int ew = warp & 3, row = threadIdx.x & 127;
@@ -771,7 +805,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       const bool any = u.t0 < u.t1;
       if (!any) live = false;
       if (any) {
-        if (!(ok = warp_wait(&bars[Lay::ACCF], units & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::ACCF], units & 1, abort_flag, to))) break;
         tc_fence_after();
       }
       const uint32_t t = tmem + (uint32_t(ew * 32) << 16);
@@ -815,7 +849,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ P^T, dS^T
-    const int g = warp >> 2, row = threadIdx.x & 127;
+    const int g = warp >> 2;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + 64 * g, tP = tmem + lanes + 128 + 64 * g;
     const float c2 = args.scale_log2;
@@ -830,8 +864,8 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       for (int t = u.t0; t < u.t1; ++t, ++e) {
         const uint32_t s = e & 1;
         const uint32_t vec = sbase + Lay::VEC_OFF + s * 1024 + g * 256;
-        if (!(ok = warp_wait(&bars[Lay::VECF + s], (e >> 1) & 1, abort_flag, to))) break;
-        if (!(ok = warp_wait(&bars[Lay::SF], e & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::VECF + s], (e >> 1) & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::SF], e & 1, abort_flag, to))) break;
         tc_fence_after();
         float p[64];
         if (!idle) {
@@ -865,7 +899,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Lay::PF]);
-        if (!(ok = warp_wait(&bars[Lay::DPF], e & 1, abort_flag, to))) break;
+        if (!(ok = cross_warp_wait(&bars[Lay::DPF], e & 1, abort_flag, to))) break;
         tc_fence_after();
         if (!idle) {
           uint32_t v[2][16];

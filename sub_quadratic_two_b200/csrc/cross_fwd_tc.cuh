@@ -16,7 +16,7 @@
 //   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies
 //                   there may be NaN or infinite, and P = 0 times NaN is NaN)
 // TMEM (512 columns): S of job x at [128x, 128x+128), O at [256 + D x, ...). P overwrites S in
-// place as packed bf16 and goes to the tensor core in two halves of 64 keys.
+// place as packed bf16.
 // The order of the products is S0(0) S1(0) | PV0(0) S0(1) | PV1(0) S1(1) | ...: the jobs take
 // turns, and while the tensor core works on one, the other's softmax runs. (An issuing thread
 // per job let the two fall in step, products against products and softmax against softmax:
@@ -66,7 +66,7 @@ struct CrossFwdLayout {
   static constexpr int NS = (NKV + 2) / 2;
   static constexpr int NB = NKV > 2 * NS ? NKV : 2 * NS;  // ring barriers of each kind
   static constexpr int BAR_OFF = (NQ + NKV) * TILE;
-  static constexpr int QF = 0, KVF = QF + NQ, KVE = KVF + NB, RDY = KVE + NB, SF = RDY + NB, PF = SF + 2, OF = PF + 4,
+  static constexpr int QF = 0, KVF = QF + NQ, KVE = KVF + NB, RDY = KVE + NB, SF = RDY + NB, PF = SF + 2, OF = PF + 2,
                        OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 2, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         uint32_t e[2] = {0, 0};
         auto load = [&](int x, const CUtensorMap* m, int row, int h, int b) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
-          if (!mbar_wait_inline(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
+          if (!cross_wait(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
           mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         // masked scores are replaced, so key tiles are passed on as they are
         auto pass = [&](int x, bool value, int b, int row, int limit) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
-          const bool ok = mbar_wait_inline(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
+          const bool ok = cross_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
           if (!__all_sync(0xffffffffu, ok)) return false;
           if (value) {
             uint32_t w[4];
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, 16, 1024),
                      v0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, kCrossBlk, 1024);
       auto wait = [&](int bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_inline(&bars[bar], parity, abort_flag, to)) != 0;
+        return cross_warp_wait(&bars[bar], parity, abort_flag, to);
       };
       const bool own = ring.count == 2;
       // ring places as slot | phase << 8, so that no step divides
@@ -226,51 +226,54 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       };
       // job x: its pending block (scores issued, P V still to come), that block's value tile and
       // place in the job; parity of its P V products; jobs begun; parities of its query slots
-      bool pend[2] = {false, false}, pfirst[2], plast[2], pnew[2], pdone[2];
+      bool pend[2] = {}, pfirst[2] = {}, plast[2] = {}, pnew[2] = {}, pdone[2] = {};
       uint32_t vpos[2] = {0, 0}, ppar[2] = {0, 0}, jobs[2] = {0, 0}, quse[2] = {0, 0};
       uint32_t kpos = 0, slot = 0;
       bool ok = true;
       auto step = [&](auto X, bool scores, bool first, bool last, bool two) -> bool {
         constexpr int x = decltype(X)::value;
         const uint32_t ts = tm + 128 * x, tacc = tm + 256 + D * x;
-        if (pend[x]) {  // P V of the block before
-          const uint32_t s = vpos[x] & 255u;
-          const uint64_t va = v0 + s * (Lay::TILE >> 4);
-          if (pnew[x] && !wait(FULL + s, vpos[x] >> 8)) return false;
+        // everything but P is there by now or comes soon: waited for first, so that the products
+        // below follow each other once P is
+        const uint32_t sv = vpos[x] & 255u;
+        const bool pv = pend[x], first_pv = pfirst[x], last_pv = plast[x], done_pv = pdone[x];
+        if (pv) {
+          if (pnew[x] && !wait(FULL + sv, vpos[x] >> 8)) return false;
           // the job's first product overwrites O: the epilogue has drained the last job's
-          if (pfirst[x]) {
+          if (first_pv) {
             if (jobs[x] > 0 && !wait(Lay::OE + x, (jobs[x] - 1) & 1)) return false;
             ++jobs[x];
           }
+        }
+        const bool fresh = own || x == 0, done = own || x == 1 || !two;
+        if (scores) {
+          if (fresh) {
+            kpos = next(own ? x : 0);
+            vpos[x] = next(own ? x : 0);
+            if (!wait(FULL + (kpos & 255u), kpos >> 8)) return false;
+          } else {
+            vpos[x] = vpos[0];
+          }
+          if (first) {
+            if (!wait(Lay::QF + slot + x, (quse[x] >> (slot >> 1)) & 1)) return false;
+            quse[x] ^= 1u << (slot >> 1);
+          }
+        }
+        if (pv) {  // P V of the block before
+          const uint64_t va = v0 + sv * (Lay::TILE >> 4);
           if (!wait(Lay::PF + x, ppar[x])) return false;
           tc_fence_after();
-          mma_ts_by(el, tacc, ts, va, id_o, pfirst[x] ? 0u : 1u);
+          mma_ts_by(el, tacc, ts, va, id_o, first_pv ? 0u : 1u);
 #pragma unroll
-          for (int kk = 1; kk < 4; ++kk) mma_ts_by(el, tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-          if (!wait(Lay::PF + 2 + x, ppar[x])) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk) mma_ts_by(el, tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
-          if (pdone[x]) tc_commit_by(el, &bars[Lay::KVE + s]);
-          if (plast[x]) tc_commit_by(el, &bars[Lay::OF + x]);
+          for (int kk = 1; kk < 8; ++kk) mma_ts_by(el, tacc, ts + kk * 8, va + kk * (2048 >> 4), id_o, 1u);
+          if (done_pv) tc_commit_by(el, &bars[Lay::KVE + sv]);
+          if (last_pv) tc_commit_by(el, &bars[Lay::OF + x]);
           ppar[x] ^= 1u;
           pend[x] = false;
         }
         if (!scores) return true;
         // S overwrites the columns that the P V above reads P from: the tensor core runs the
         // products of one thread in issue order
-        const bool fresh = own || x == 0, done = own || x == 1 || !two;
-        if (fresh) {
-          kpos = next(own ? x : 0);
-          vpos[x] = next(own ? x : 0);
-          if (!wait(FULL + (kpos & 255u), kpos >> 8)) return false;
-        } else {
-          vpos[x] = vpos[0];
-        }
-        if (first) {
-          if (!wait(Lay::QF + slot + x, (quse[x] >> (slot >> 1)) & 1)) return false;
-          quse[x] ^= 1u << (slot >> 1);
-        }
         tc_fence_after();
         const uint64_t qa = q0 + (slot + x) * (Lay::TILE >> 4), ka = k0 + (kpos & 255u) * (Lay::TILE >> 4);
 #pragma unroll
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     uint32_t qused = 0, qpar = 0;   // per query slot: ever loaded, parity of its loads
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
+      return cross_warp_wait(bar, parity, abort_flag, to);
     };
     // the query tile of job x of item i into slot s, where there is such a job
     auto load_q = [&](long long i, int x, uint32_t s) {
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           // the statistics of every warp's rows are read before the next query tile comes
           if (threadIdx.x == 256) {
-            ok = mbar_wait_inline(&bars[Lay::ST + x], job & 1, abort_flag, to);
+            ok = cross_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
             if (ok) load_q(i + 2ll * gridDim.x, x, s);
           }
           ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           mbar_arrive(&bars[Lay::OE + x]);
         }
         if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = mbar_wait_inline(&bars[Lay::ST + x], job & 1, abort_flag, to);
+          ok = cross_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
 #pragma unroll
           for (int c = 0; ok && c < DH; ++c)
             tma_store_4d(&maps.o, tile + c * kCrossBlk, c * 64, qt * 128, it.h * args.o_h, it.b * args.o_b);
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     uint32_t sc = 0, jobs = 0;
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, to)) != 0;
+      return cross_warp_wait(bar, parity, abort_flag, to);
     };
     uint32_t item = 0;
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
@@ -478,7 +481,6 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           tc_fence_before();
           if (lane == 0) {
             mbar_arrive(&bars[Lay::PF + x]);
-            mbar_arrive(&bars[Lay::PF + 2 + x]);
           }
           continue;
         }
@@ -539,8 +541,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         const float neg = m_use == -INFINITY ? 0.f : -m_use * c2;  // a row without keys: every exponent is -inf
         const uint64_t neg2 = f2(neg, neg);
         uint64_t sum[2] = {0ull, 0ull};
-        // P packed over the columns that the scores lay in, 32 keys at a time; the first 64 keys are
-        // handed over while the third chunk's exponentials run, so that their stores are not waited for
+        // P packed over the columns that the scores lay in, 32 keys at a time, handed over whole (in
+        // two halves it took the issuer a wait more: 166.5 against 165 us at 27,280 x 512)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
@@ -552,13 +554,11 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             p[e >> 1] = pack_bf16x2(p0, p1);
           }
           tmem_st16(tS + 16 * c, p);
-          if (c >= 2) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[Lay::PF + 2 * (c - 2) + x]);
-          }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::PF + x]);
         const uint64_t s2 = fadd2(sum[0], sum[1]);
         l_run = l_run * alpha + (f2_lo(s2) + f2_hi(s2));
         m_run = m_use;

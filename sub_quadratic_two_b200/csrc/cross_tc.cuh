@@ -91,10 +91,43 @@ __device__ __forceinline__ void st_shared_f2(uint32_t addr, float a, float b) {
 __device__ __forceinline__ void ld_shared_f2(uint32_t addr, float& a, float& b) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
 }
+
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// Bounded wait of these kernels (as mbar_wait), in line: a kernel that moves registers between its
+// warps (regs_take, regs_give) must not call functions, or ptxas holds every path to the launch's
+// share. Without a suspend-time hint a wait that finds its phase complete takes 65 cycles, with one 96.
+__device__ __forceinline__ bool cross_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool cross_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+  if (__builtin_expect(cross_try_wait(bar, parity), 1)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (;;) {
+    if (cross_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > timeout_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// By a whole warp; the answer is the same in every lane.
+__device__ __forceinline__ bool cross_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, cross_wait(bar, parity, abort, timeout_ns)) != 0;
 }
 
 // ---- issue by a whole warp: the warp stays together (so that addresses and descriptors can live

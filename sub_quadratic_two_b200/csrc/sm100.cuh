@@ -79,23 +79,6 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
   }
 }
 
-// The same wait with its loop in line: a kernel that moves registers between its warps
-// (regs_take, regs_give) must not call functions, or ptxas holds every path to the launch's share.
-__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                 uint64_t timeout_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > timeout_ns) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
 // Bounded wait that ignores the abort flag: used on the way out, to let copies
 // and tensor-core work already in flight finish before the CTA releases memory.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
