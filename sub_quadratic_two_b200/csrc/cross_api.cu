@@ -11,8 +11,8 @@
 
 #include "squad.h"
 #include "cross_bwd_tc.cuh"
+#include "cross_f32.cuh"
 #include "cross_fwd_tc.cuh"
-#include "cross_simt.cuh"
 #include "geometry.h"
 #include "host_state.h"
 #include "rotary.cuh"
@@ -103,42 +103,73 @@ sq::CrossArgs cross_args(const squad_cross_desc* d, const void* q, const void* k
   return a;
 }
 
-dim3 row_grid(const sq::CrossArgs& a, int rows, int heads) {
-  return dim3(unsigned((rows + sq::kSimtWarps - 1) / sq::kSimtWarps), unsigned(heads), unsigned(a.B));
-}
+constexpr int kMaxDevices = 64;
 
-template <typename T, int DPL>
-squad_status simt_cross_fwd(const sq::CrossArgs& a, cudaStream_t st) {
-  sq::cross_simt_fwd_kernel<T, DPL><<<row_grid(a, a.n, a.heads), sq::kSimtWarps * 32, 0, st>>>(a);
-  SQ_CUDA(cudaGetLastError());
-  return SQUAD_OK;
-}
-
-template <typename T, int DPL>
-squad_status simt_cross_bwd(const sq::CrossArgs& a, cudaStream_t st) {
-  sq::cross_simt_dq_kernel<T, DPL><<<row_grid(a, a.n, a.heads), sq::kSimtWarps * 32, 0, st>>>(a);
-  SQ_CUDA(cudaGetLastError());
-  sq::cross_simt_dkdv_kernel<T, DPL><<<row_grid(a, a.m, a.kv_heads), sq::kSimtWarps * 32, 0, st>>>(a);
-  SQ_CUDA(cudaGetLastError());
-  return SQUAD_OK;
-}
-
-template <typename T, bool BWD>
-squad_status simt_cross(const sq::CrossArgs& a, cudaStream_t st) {
-#define SQ_DPL(N) \
-  case N:         \
-    return BWD ? simt_cross_bwd<T, N>(a, st) : simt_cross_fwd<T, N>(a, st)
-  switch (a.d / 32) {
-    SQ_DPL(1);
-    SQ_DPL(2);
-    SQ_DPL(3);
-    SQ_DPL(4);
-    SQ_DPL(5);
-    SQ_DPL(6);
-    SQ_DPL(7);
-    SQ_DPL(8);
+// The attribute is set once per kernel and device; a repeated set by two threads is harmless.
+template <typename K>
+squad_status allow_smem(K kern, int bytes, const sq::HostDevice& dev, std::atomic<bool>* done) {
+  if (!done[dev.device].load(std::memory_order_acquire)) {
+    SQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done[dev.device].store(true, std::memory_order_release);
   }
-#undef SQ_DPL
+  return SQUAD_OK;
+}
+
+// ---------------------------------------------------------------- fp32
+
+template <int D>
+squad_status f32_cross_fwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  auto kern = sq::cross_f32_fwd_kernel<D>;
+  squad_status s = allow_smem(kern, sq::F32Layout<D>::FWD, dev, done);
+  if (s != SQUAD_OK) return s;
+  const dim3 grid(unsigned((a.n + sq::kF32Rows - 1) / sq::kF32Rows), unsigned(a.heads), unsigned(a.B));
+  kern<<<grid, sq::kF32Threads, sq::F32Layout<D>::FWD, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
+template <int D>
+squad_status f32_cross_bwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+  static std::atomic<bool> done_q[kMaxDevices], done_kv[kMaxDevices];
+  auto dq = sq::cross_f32_dq_kernel<D>;
+  auto dkv = sq::cross_f32_dkdv_kernel<D>;
+  squad_status s;
+  if ((s = allow_smem(dq, sq::F32Layout<D>::DQ, dev, done_q)) != SQUAD_OK) return s;
+  if ((s = allow_smem(dkv, sq::F32Layout<D>::DKV, dev, done_kv)) != SQUAD_OK) return s;
+  const dim3 gq(unsigned((a.n + sq::kF32Rows - 1) / sq::kF32Rows), unsigned(a.heads), unsigned(a.B));
+  dq<<<gq, sq::kF32Threads, sq::F32Layout<D>::DQ, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  const dim3 gk(unsigned((a.m + sq::kF32Rows - 1) / sq::kF32Rows * a.splits), unsigned(a.kv_heads), unsigned(a.B));
+  dkv<<<gk, sq::kF32Threads, sq::F32Layout<D>::DKV, st>>>(a);
+  SQ_CUDA(cudaGetLastError());
+  if (a.splits > 1) {
+    const long long rows = (long long)a.B * a.kv_heads * a.m;
+    const dim3 grid(unsigned((rows * (D / 4) + 255) / 256), 2);
+    sq::cross_join_grads_kernel<float><<<grid, 256, 0, st>>>(a.part, a.splits, rows, a.m, a.kv_heads, a.m, D, rows,
+                                                             static_cast<float*>(a.dk), a.sdk,
+                                                             static_cast<float*>(a.dv), a.sdv);
+    SQ_CUDA(cudaGetLastError());
+  }
+  return SQUAD_OK;
+}
+
+template <bool BWD>
+squad_status f32_cross(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+#define SQ_D(N) \
+  case N:       \
+    return BWD ? f32_cross_bwd<N>(dev, a, st) : f32_cross_fwd<N>(dev, a, st)
+  switch (a.d) {
+    SQ_D(32);
+    SQ_D(64);
+    SQ_D(96);
+    SQ_D(128);
+    SQ_D(160);
+    SQ_D(192);
+    SQ_D(224);
+    SQ_D(256);
+  }
+#undef SQ_D
   return SQUAD_ERR_UNSUPPORTED;
 }
 
@@ -156,18 +187,6 @@ squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void
                                *mb ? uint64_t(st.b) * 2 : row};
   const uint32_t box[4] = {64, 128, 1, 1};
   return sq::host_encode_bf16(map, dev.device, 4, base, dims, strides, box);
-}
-
-constexpr int kMaxDevices = 64;
-
-// The attribute is set once per kernel and device; a repeated set by two threads is harmless.
-template <typename K>
-squad_status allow_smem(K kern, int bytes, const sq::HostDevice& dev, std::atomic<bool>* done) {
-  if (!done[dev.device].load(std::memory_order_acquire)) {
-    SQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    done[dev.device].store(true, std::memory_order_release);
-  }
-  return SQUAD_OK;
 }
 
 struct FwdWs {
@@ -255,11 +274,13 @@ BwdWs bwd_workspace(const squad_cross_desc* d) {
   w.splits = 1;
   w.part = bwd_rowvec_bytes(d);
   w.total = w.part;
-  if (d->dtype != SQUAD_BF16) return w;
-  const long long units = (long long)d->B * d->kv_heads * ((d->m + 127) / 128);
-  const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + 127) / 128);
+  const bool tc = d->dtype == SQUAD_BF16;
+  const int keys = tc ? 128 : sq::kF32Rows, queries = tc ? 128 : sq::kF32Cols;
+  const long long units = (long long)d->B * d->kv_heads * ((d->m + keys - 1) / keys);
+  const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + queries - 1) / queries);
   w.splits = sq::cross_dkv_splits(units, int(tiles));
-  if (w.splits > 1) w.total += align256(size_t(2) * w.splits * units * 128 * d->d * sizeof(float));
+  const size_t rows = tc ? size_t(units) * 128 : size_t(d->B) * d->kv_heads * d->m;
+  if (w.splits > 1) w.total += align256(size_t(2) * w.splits * rows * d->d * sizeof(float));
   return w;
 }
 
@@ -281,9 +302,9 @@ squad_status launch_cross_bwd(const sq::HostDevice& dev, const sq::CrossBwdMaps&
   if (a.splits > 1) {
     const long long rows = (long long)a.B * a.kv_heads * a.m;
     const dim3 grid(unsigned((rows * (D / 4) + 255) / 256), 2);
-    sq::cross_join_grads_kernel<D><<<grid, 256, 0, st>>>(a.part, a.splits,
-                                                         (long long)a.B * a.kv_heads * a.kblocks * 128, a.kblocks * 128,
-                                                         a.kv_heads, a.m, rows, a.dk, a.sdk, a.dv, a.sdv);
+    sq::cross_join_grads_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
+        a.part, a.splits, (long long)a.B * a.kv_heads * a.kblocks * 128, a.kblocks * 128, a.kv_heads, a.m, D, rows, a.dk,
+        a.sdk, a.dv, a.sdv);
     SQ_CUDA(cudaGetLastError());
   }
   return SQUAD_OK;
@@ -374,7 +395,7 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
   a.o = o;
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, workspace, st) : simt_cross<float, false>(a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, workspace, st) : f32_cross<false>(dev, a, st);
 }
 
 squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
@@ -403,8 +424,11 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   a.dk = dk;
   a.dv = dv;
   a.Drow = static_cast<float*>(workspace);
+  const BwdWs w = bwd_workspace(desc);
+  a.splits = w.splits;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : simt_cross<float, true>(a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : f32_cross<true>(dev, a, st);
 }
 
 // ---------------------------------------------------------------- rotary positions

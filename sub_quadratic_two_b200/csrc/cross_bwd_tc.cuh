@@ -947,13 +947,14 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   }
 }
 
-// dk, dv = sum of their parts in order of the splits, 4 channels per thread.
-template <int D>
+// dk, dv = sum of their parts in order of the splits, 4 channels per thread. Rows of the parts:
+// mpad for each (b, kv head).
+template <typename T>
 __global__ void __launch_bounds__(256) cross_join_grads_kernel(const float* __restrict__ part, int splits,
                                                                long long part_rows, int mpad, int kv_heads, int m,
-                                                               long long rows, __nv_bfloat16* dk, CrossStride sdk,
-                                                               __nv_bfloat16* dv, CrossStride sdv) {
-  constexpr int C = D / 4;
+                                                               int D, long long rows, T* dk, CrossStride sdk, T* dv,
+                                                               CrossStride sdv) {
+  const int C = D / 4;
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long r = id / C;  // (b, kv head, key) of the unpadded rows
   if (r >= rows) return;
@@ -970,8 +971,11 @@ __global__ void __launch_bounds__(256) cross_join_grads_kernel(const float* __re
     a.w += x.w;
   }
   const CrossStride& st = which ? sdv : sdk;
-  *reinterpret_cast<uint2*>((which ? dv : dk) + b * st.b + h * st.h + j * st.n + c) =
-      make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  T* out = (which ? dv : dk) + b * st.b + h * st.h + j * st.n + c;
+  if (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  else
+    *reinterpret_cast<float4*>(out) = a;
 }
 
 }  // namespace sq

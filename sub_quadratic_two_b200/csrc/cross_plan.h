@@ -96,10 +96,11 @@ SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   return r;
 }
 
-// How many parts the queries of a key tile are cut into (dk, dv kernel): `units` key tiles of
-// `tiles` query tiles each over the SMs, in the time of one query tile (about 1.1 us at d = 128):
-// rounds of units * s over the SMs, each ceil(tiles / s) tiles and 1.5 to fill and drain, plus,
-// for s > 1, the join kernel (2) and its traffic (0.05 for each part of 128 keys).
+// How many parts the queries of a key tile are cut into (dk, dv kernels): `units` key tiles of
+// `tiles` query tiles each over the SMs, in the time of one query tile
+// (about 1.1 us for the tensor cores at d = 128): rounds of units * s over the SMs, each
+// ceil(tiles / s) tiles and 1.5 to fill and drain, plus, for s > 1, the join kernel (2) and its
+// traffic (0.05 for each part of 128 keys).
 inline int cross_dkv_splits(long long units, int tiles) {
   int best = 1;
   double best_cost = 0;

@@ -3,7 +3,8 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
-#include "cross_simt.cuh"
+#include "cross_args.h"
+#include "geometry.h"
 #include "sm100.cuh"
 
 namespace sq {
