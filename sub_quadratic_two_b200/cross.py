@@ -7,8 +7,8 @@ from typing import Optional
 
 import torch
 
-from . import _check, _check_aux, _dtype_code, _ptr, _stream_handle, load_library
-from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout
+from . import _check, _check_aux, _dtype_code, load_library
+from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout, on_device, raw_stream
 
 
 class SquadCrossDesc(ctypes.Structure):
@@ -17,7 +17,6 @@ class SquadCrossDesc(ctypes.Structure):
                 + [(f, SquadStrides) for f in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")])
 
 
-@lru_cache(maxsize=512)
 def _desc(q_shape, k_shape, code: int, scale: float, mask_stride: int, strides) -> SquadCrossDesc:
     B, h, n, d = q_shape
     desc = SquadCrossDesc(B, h, k_shape[1], n, k_shape[2], d, code, scale, mask_stride)
@@ -33,6 +32,10 @@ def _workspace(q_shape, k_shape, code: int, which: int) -> int:
     _check(load_library().squad_cross_workspace_size(ctypes.byref(desc), which, ctypes.byref(nb)),
            "squad_cross_workspace_size")
     return int(nb.value)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _check_cross(q, k, v, kv_lens, key_mask) -> int:
@@ -58,6 +61,30 @@ def _check_cross(q, k, v, kv_lens, key_mask) -> int:
     return step
 
 
+def _kind(t: Optional[torch.Tensor]):
+    """What the checks look at in a tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+_calls = {}  # (what the checks look at, scale) -> what a call needs besides its pointers
+
+
+def _call(tensors, kv_lens, key_mask, scale, build):
+    """The checked call of these kinds of tensors, made by build() the first time."""
+    try:
+        key = (tuple(map(_kind, tensors)), _kind(kv_lens), _kind(key_mask), scale)
+        return _calls[key]
+    except KeyError:
+        pass
+    except (AttributeError, TypeError):  # not a tensor: the checks say which
+        return build()
+    call = build()
+    if len(_calls) >= 1024:
+        _calls.clear()
+    _calls[key] = call
+    return call
+
+
 def cross_workspace_size(q: torch.Tensor, k: torch.Tensor, which: int) -> int:
     """Bytes of device workspace the forward (which = 0) or backward (1) of these shapes needs."""
     return _workspace(tuple(q.shape), tuple(k.shape), _dtype_code(q), which)
@@ -70,58 +97,69 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
 
     o lies in memory as q does (token-major or head-major), or in ``out``.
     """
-    lib = load_library()
-    step = _check_cross(q, k, v, kv_lens, key_mask)
-    if out is not None:
-        check_strided(("q", q), ("out", out))
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
+
+    def build():
+        step = _check_cross(q, k, v, kv_lens, key_mask)
+        if out is not None:
+            check_strided(("q", q), ("out", out))
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        o = out if out is not None else empty_like_layout(q)
+        code = _dtype_code(q)
+        if q.numel() == 0 or k.numel() == 0:
+            return None, 0
+        desc = _desc(q.shape, k.shape, code, float(scale or 0.0), step, (q.stride(), k.stride(), v.stride(), o.stride()))
+        return desc, _workspace(tuple(q.shape), tuple(k.shape), code, 0)
+
+    desc, nb = _call((q, k, v, out), kv_lens, key_mask, scale, build)
     o = empty_like_layout(q) if out is None else out
     lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32) if save else None
-    if q.numel() == 0 or k.numel() == 0:  # no query, or no key for any of them
+    if desc is None:  # no query, or no key for any of them
         o.zero_()
         if save:
             lse.fill_(float("-inf"))
         return o, lse
-    code = _dtype_code(q)
-    nb = _workspace(tuple(q.shape), tuple(k.shape), code, 0)
     ws = torch.empty(nb, device=q.device, dtype=torch.uint8) if nb else None
-    desc = _desc(tuple(q.shape), tuple(k.shape), code, float(scale or 0.0), step,
-                 (q.stride(), k.stride(), v.stride(), o.stride()))
-    with torch.cuda.device(q.device):
-        _check(lib.squad_cross_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(key_mask),
-                                   _ptr(o), _ptr(lse), _ptr(ws), nb, _stream_handle(None, q.device)),
-               "squad_cross_fwd")
+    with on_device(q.device):
+        _check(load_library().squad_cross_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                              _at(kv_lens), _at(key_mask), o.data_ptr(), _at(lse), _at(ws), nb,
+                                              raw_stream(q.device)), "squad_cross_fwd")
     return o, lse
 
 
 def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_lens: Optional[torch.Tensor] = None,
                     key_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """Backward through the C ABI. Returns (dq, dk, dv), each lying in memory as q, k and v do."""
-    lib = load_library()
-    step = _check_cross(q, k, v, kv_lens, key_mask)
-    check_strided(("q", q), ("o", o), ("dout", dout))
-    if o.shape != q.shape or dout.shape != q.shape:
-        raise ValueError("o and dout must have q's shape")
-    _check_aux(lse, q.shape[:3], torch.float32, q.device, "lse")
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
-    dq, dk, dv = (empty_like_layout(t) for t in (q, k, v))
-    if q.numel() == 0 or k.numel() == 0:
+
+    def build():
+        step = _check_cross(q, k, v, kv_lens, key_mask)
+        check_strided(("q", q), ("o", o), ("dout", dout))
+        if o.shape != q.shape or dout.shape != q.shape:
+            raise ValueError("o and dout must have q's shape")
+        _check_aux(lse, q.shape[:3], torch.float32, q.device, "lse")
+        code = _dtype_code(q)
+        if q.numel() == 0 or k.numel() == 0:
+            return None, 0
+        strides = [t.stride() for t in (q, k, v, o, dout)] + [empty_like_layout(t).stride() for t in (q, k, v)]
+        return (_desc(q.shape, k.shape, code, float(scale or 0.0), step, strides),
+                _workspace(tuple(q.shape), tuple(k.shape), code, 1))
+
+    desc, nb = _call((q, k, v, o, lse, dout), kv_lens, key_mask, scale, build)
+    dq, dk, dv = empty_like_layout(q), empty_like_layout(k), empty_like_layout(v)
+    if desc is None:
         return dq.zero_(), dk.zero_(), dv.zero_()
-    code = _dtype_code(q)
-    nb = _workspace(tuple(q.shape), tuple(k.shape), code, 1)
     ws = torch.empty(nb, device=q.device, dtype=torch.uint8)
-    desc = _desc(tuple(q.shape), tuple(k.shape), code, float(scale or 0.0), step,
-                 tuple(t.stride() for t in (q, k, v, o, dout, dq, dk, dv)))
-    with torch.cuda.device(q.device):
-        _check(lib.squad_cross_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(key_mask),
-                                   _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), nb,
-                                   _stream_handle(None, q.device)), "squad_cross_bwd")
+    with on_device(q.device):
+        _check(load_library().squad_cross_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                              _at(kv_lens), _at(key_mask), o.data_ptr(), lse.data_ptr(),
+                                              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                              ws.data_ptr(), nb, raw_stream(q.device)), "squad_cross_bwd")
     return dq, dk, dv
 
 
@@ -152,4 +190,6 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Op
     kv_lens: [B] int32, the states of each batch row that count; key_mask: [B, m] (or [1, m]) bool, True
     where a state counts. A query with no state left gets zeros and gives no gradient.
     """
-    return _CrossAttention.apply(q, k, v, scale, kv_lens, key_mask)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return _CrossAttention.apply(q, k, v, scale, kv_lens, key_mask)
+    return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save=False)[0]

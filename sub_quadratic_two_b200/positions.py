@@ -6,14 +6,14 @@ and `attention` and `attention_multi` take a plan as `rotary=`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
-from functools import lru_cache
 from typing import Optional, Sequence, Tuple
 
 import torch
 
-from . import _check, _dtype_code, _ptr, _stream_handle, load_library
+from . import _check, _dtype_code, load_library
 
 PAIRINGS = {"adjacent": 0, "half": 1}
 
@@ -26,8 +26,17 @@ class SquadRotaryDesc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in ("B", "d", "T", "H", "W", "cT", "cH", "cW", "dtype", "pairing", "inverse")]
 
 
-def strides_of(t: torch.Tensor) -> SquadStrides:
-    return SquadStrides(*t.stride()[:3])
+_nothing = contextlib.nullcontext()
+
+
+def on_device(dev: torch.device):
+    """A context in which dev is the current device (nothing to do where it is, the common case)."""
+    return _nothing if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def raw_stream(dev: torch.device) -> int:
+    """The handle of dev's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def token_major(t: torch.Tensor) -> bool:
@@ -37,6 +46,8 @@ def token_major(t: torch.Tensor) -> bool:
 
 def empty_like_layout(t: torch.Tensor) -> torch.Tensor:
     """A dense tensor of t's shape, token-major where t is, else head-major."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
     B, h, n, d = t.shape
     if token_major(t):
         return torch.empty((B, n, h, d), device=t.device, dtype=t.dtype).transpose(1, 2)
@@ -86,6 +97,8 @@ class Rotary:
     pairing: str = "adjacent"
 
     def __post_init__(self):
+        object.__setattr__(self, "grid", tuple(self.grid))
+        object.__setattr__(self, "axes", tuple(self.axes))
         if len(self.grid) != 3 or len(self.axes) != 3 or min(self.grid) < 1 or min(self.axes) < 0:
             raise ValueError("grid and axes are (time, height, width): positive sizes, channels of each")
         if any(c % 2 for c in self.axes):
@@ -122,22 +135,15 @@ def rotary_plan(grid: Sequence[int], d: int, axes: Optional[Sequence[int]] = Non
     return Rotary(grid, axes, torch.cat(parts).float().contiguous().to(dev), pairing)
 
 
-@lru_cache(maxsize=256)
-def _rotary_desc(B: int, d: int, grid, axes, code: int, pairing: str, inverse: bool) -> SquadRotaryDesc:
-    return SquadRotaryDesc(B, d, *grid, *axes, code, PAIRINGS[pairing], int(inverse))
+_calls = {}  # kinds of the tensors and the plan -> the checked arguments of squad_rotary besides its pointers
 
 
-def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
-                 out: Optional[Sequence[torch.Tensor]] = None, stream: Optional[torch.cuda.Stream] = None):
-    """One or two tensors [B, heads, T*H*W, d] through the C ABI in one launch; returns the list of outputs.
-
-    inverse turns by the opposite angles. out: tensors to write (any strides of whole 16-byte steps; an input
-    itself for the rotation in place), else contiguous ones are made.
-    """
-    lib = load_library()
-    check_strided(*[(f"xs[{i}]", x) for i, x in enumerate(xs)])
-    if not 1 <= len(xs) <= 2:
+def _rotary_call(xs, rot: Rotary, inverse: bool, ys):
+    """Checks a call; returns its arguments that depend on the geometry alone."""
+    c = len(xs)
+    if not 1 <= c <= 2:
         raise ValueError("one or two tensors")
+    check_strided(*[(f"xs[{i}]", x) for i, x in enumerate(xs)])
     ref = xs[0]
     B, _, n, d = ref.shape
     T, H, W = rot.grid
@@ -148,25 +154,50 @@ def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
         raise ValueError(f"n={n} but T*H*W={T * H * W}")
     if rot.table.device != ref.device:
         raise ValueError(f"the rotary table must be on {ref.device}")
-    if out is not None:
-        check_strided(("xs[0]", ref), *[(f"out[{i}]", y) for i, y in enumerate(out)])
-        if len(out) != len(xs) or any(x.shape != y.shape for x, y in zip(xs, out)):
-            raise ValueError("out must hold one tensor of each input's shape")
+    if len(ys) != c:
+        raise ValueError("out must hold one tensor for each input")
+    check_strided(("xs[0]", ref), *[(f"out[{i}]", y) for i, y in enumerate(ys)])
+    if any(x.shape != y.shape for x, y in zip(xs, ys)):
+        raise ValueError("out must hold one tensor of each input's shape")
+    desc = SquadRotaryDesc(B, d, *rot.grid, *rot.axes, _dtype_code(ref), PAIRINGS[rot.pairing], int(inverse))
+    return (desc, c, (ctypes.c_int * c)(*[x.shape[1] for x in xs]),
+            (SquadStrides * c)(*[SquadStrides(*x.stride()[:3]) for x in xs]),
+            (SquadStrides * c)(*[SquadStrides(*y.stride()[:3]) for y in ys]), ctypes.c_void_p * c)
+
+
+def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
+                 out: Optional[Sequence[torch.Tensor]] = None, stream: Optional[torch.cuda.Stream] = None):
+    """One or two tensors [B, heads, T*H*W, d] through the C ABI in one launch; returns the list of outputs.
+
+    inverse turns by the opposite angles. out: tensors to write (any strides of whole 16-byte steps; an input
+    itself for the rotation in place), else contiguous ones are made.
+    """
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_rotary(xs, rot, inverse, out)
-    ys = [torch.empty(x.shape, device=x.device, dtype=x.dtype) for x in xs] if out is None else list(out)
-    if B == 0 or any(x.shape[1] == 0 for x in xs):
+    if out is None:
+        ys = [torch.empty(x.shape, device=x.device, dtype=x.dtype) for x in xs]
+    else:
+        ys = list(out)
+    if not xs:
+        raise ValueError("one or two tensors")
+    ref = xs[0]
+    key = (tuple([(x.shape, x.stride(), x.dtype, x.device) for x in xs]),
+           tuple([(y.shape, y.stride(), y.dtype, y.device) for y in ys]),
+           rot.grid, rot.axes, rot.pairing, rot.table.device, inverse)
+    call = _calls.get(key)
+    if call is None:
+        call = _rotary_call(xs, rot, inverse, ys)
+        if len(_calls) >= 1024:
+            _calls.clear()
+        _calls[key] = call
+    if ref.shape[0] == 0 or any([x.shape[1] == 0 for x in xs]):
         return ys
-    c = len(xs)
-    desc = _rotary_desc(B, d, tuple(rot.grid), tuple(rot.axes), _dtype_code(ref), rot.pairing, bool(inverse))
-    with torch.cuda.device(ref.device):
-        _check(lib.squad_rotary(ctypes.byref(desc), c, (ctypes.c_int * c)(*[x.shape[1] for x in xs]),
-                                (ctypes.c_void_p * c)(*[x.data_ptr() for x in xs]),
-                                (SquadStrides * c)(*[strides_of(x) for x in xs]),
-                                (ctypes.c_void_p * c)(*[y.data_ptr() for y in ys]),
-                                (SquadStrides * c)(*[strides_of(y) for y in ys]), _ptr(rot.table),
-                                _stream_handle(None, ref.device)), "squad_rotary")
+    desc, c, heads, sx, sy, pointers = call
+    with on_device(ref.device):
+        _check(load_library().squad_rotary(ctypes.byref(desc), c, heads, pointers(*[x.data_ptr() for x in xs]), sx,
+                                           pointers(*[y.data_ptr() for y in ys]), sy, rot.table.data_ptr(),
+                                           raw_stream(ref.device)), "squad_rotary")
     return ys
 
 
@@ -199,6 +230,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary):
     k may have its own number of heads, or be None (then None comes back in its place). Differentiable; the
     gradients come in the memory layout of q and k.
     """
-    if k is None:
-        return _Rotary.apply(rot, q)[0], None
-    return _Rotary.apply(rot, q, k)
+    xs = (q,) if k is None else (q, k)
+    # without a gradient to come there is nothing for autograd to record
+    ys = _Rotary.apply(rot, *xs) if torch.is_grad_enabled() and any(x.requires_grad for x in xs) else squad_rotary(xs, rot)
+    return ys[0], None if k is None else ys[1]
