@@ -175,17 +175,17 @@ squad_status f32_cross(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaSt
 
 // ---------------------------------------------------------------- tensor-core forward (bf16)
 
-// 4-D map (channel, row, head, batch) over a strided tensor, boxes of 64 channels x 128 rows.
+// 4-D map (channel, row, head, batch) over a strided tensor, boxes of 64 channels x `rows` rows.
 // Extents that are 1 or broadcast (stride 0) are left out: their coordinate is times mb, mh.
 squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void* base, const squad_strides& st, int B,
-                         int h, int n, int d, int* mb, int* mh) {
+                         int h, int n, int d, int* mb, int* mh, uint32_t rows = 128) {
   const uint64_t row = uint64_t(d) * 2;
   *mb = B > 1 && st.b != 0;
   *mh = h > 1 && st.h != 0;
   const uint64_t dims[4] = {uint64_t(d), uint64_t(n), *mh ? uint64_t(h) : 1, *mb ? uint64_t(B) : 1};
   const uint64_t strides[3] = {n > 1 ? uint64_t(st.n) * 2 : row, *mh ? uint64_t(st.h) * 2 : row,
                                *mb ? uint64_t(st.b) * 2 : row};
-  const uint32_t box[4] = {64, 128, 1, 1};
+  const uint32_t box[4] = {64, rows, 1, 1};
   return sq::host_encode_bf16(map, dev.device, 4, base, dims, strides, box);
 }
 
@@ -212,8 +212,7 @@ squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& ma
   static std::atomic<bool> done[kMaxDevices];
   squad_status s = allow_smem(kern, Lay::BYTES, dev, done);
   if (s != SQUAD_OK) return s;
-  // split keys: one item per CTA (the kernel uses the room of a second item's queries)
-  const int grid = a.plan.items < dev.sms || a.plan.splits > 1 ? a.plan.items : dev.sms;
+  const int grid = a.plan.items < dev.sms ? a.plan.items : dev.sms;
   kern<<<grid, sq::kCrossThreads, Lay::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
   return SQUAD_OK;
@@ -232,7 +231,7 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   if ((s = encode_rows(&maps.q, dev, c.q, d->q, d->B, d->heads, d->n, d->d, &a.q_b, &a.q_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.k, dev, c.k, d->k, d->B, d->kv_heads, d->m, d->d, &a.k_b, &a.k_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.v, dev, c.v, d->v, d->B, d->kv_heads, d->m, d->d, &a.v_b, &a.v_h)) != SQUAD_OK) return s;
-  if ((s = encode_rows(&maps.o, dev, c.o, d->o, d->B, d->heads, d->n, d->d, &a.o_b, &a.o_h)) != SQUAD_OK) return s;
+  if ((s = encode_rows(&maps.o, dev, c.o, d->o, d->B, d->heads, d->n, d->d, &a.o_b, &a.o_h, 32)) != SQUAD_OK) return s;
   a.mask = c.mask;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.lse = c.lse;

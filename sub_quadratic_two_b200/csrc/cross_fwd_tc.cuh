@@ -7,11 +7,11 @@
 //
 // Roles (512 threads):
 //   warps 0-3, 4-7  softmax of job 0, job 1 (thread = query row = TMEM lane)
-//   warps 8-11      epilogue: O / sum -> bf16 -> the job's Q tile (no longer needed) in shared
-//                   memory -> TMA store, so the softmax warps go on with the next item; their
-//                   first thread then loads the job's query tile of the item after next there
+//   warps 8-11      epilogue: O / sum -> bf16 -> one of the warp's two staging buffers (32 rows x 64
+//                   channels) -> TMA store, so the softmax warps go on with the next item
 //   warp 12         TMA loads of key and value tiles, K(0) V(0) K(1) V(1) ... in a ring (a ring for
 //                   each job where the keys are split)
+//   warp 15         TMA loads of query tiles: the next item's as soon as a job's last scores are made
 //   warp 13         issues every tcgen05.mma (the whole warp runs the loop, one lane's count)
 //   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies
 //                   there may be NaN or infinite, and P = 0 times NaN is NaN)
@@ -59,15 +59,20 @@ struct CrossFwdArgs {
 template <int D>
 struct CrossFwdLayout {
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NQ = 4;  // query tile of job x of the CTA's j-th item: slot 2 (j & 1) + x
-  static constexpr int NKV = D == 128 ? 3 : 8;  // ring of key and value tiles, behind the query tiles
-  // Split keys: a CTA has one item, so query slots 2 and 3 are free, and each job takes half of
-  // the tiles behind slot 1 as a ring of its own.
-  static constexpr int NS = (NKV + 2) / 2;
-  static constexpr int NB = NKV > 2 * NS ? NKV : 2 * NS;  // ring barriers of each kind
-  static constexpr int BAR_OFF = (NQ + NKV) * TILE;
-  static constexpr int QF = 0, KVF = QF + NQ, KVE = KVF + NB, RDY = KVE + NB, SF = RDY + NB, PF = SF + 2, OF = PF + 2,
-                       OE = OF + 2, LF = OE + 2, ST = LF + 4, DRAIN = ST + 2, NBAR = DRAIN + 1;
+  // Query tile of each job, two staging buffers of 64 channels, the ring of key and value tiles.
+  // Four ring tiles at d = 128: with three, a key tile waits for the values of two blocks before
+  // (the issuer waited 0.4k cycles a block for it).
+  static constexpr int STAGE_OFF = 2 * TILE;
+  static constexpr int KV_OFF = STAGE_OFF + 2 * int(kCrossBlk);
+  static constexpr int NKV = D == 128 ? 4 : 10;
+  // Split keys: each job takes half of the ring as its own. (With one ring for both, the reader of
+  // a tile would not see the phases of the tiles that the other job reads, and a wait by parity
+  // needs every phase.)
+  static constexpr int NS = NKV / 2;
+  static constexpr int STAT_OFF = KV_OFF + NKV * TILE;   // (maximum, sum) of each job's rows
+  static constexpr int BAR_OFF = STAT_OFF + 2 * 128 * 8;
+  static constexpr int QF = 0, QE = QF + 2, KVF = QE + 2, KVE = KVF + NKV, RDY = KVE + NKV, SF = RDY + NKV, PF = SF + 2,
+                       OF = PF + 2, OE = OF + 2, LF = OE + 2, LE = LF + 2, DRAIN = LE + 2, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -117,14 +122,14 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   // Rings of key and value tiles: entry n of job x (or of both) lies in slot(x, n), for the
   // use(n)-th time.
   struct Ring {
-    uint32_t size, tile0;
+    uint32_t size;
     int count;
     __device__ __forceinline__ uint32_t slot(int x, uint32_t n) const {
       return (count == 2 ? x * size : 0u) + n % size;
     }
     __device__ __forceinline__ uint32_t use(uint32_t n) const { return n / size; }
   };
-  const Ring ring = plan.splits > 1 ? Ring{uint32_t(Lay::NS), 2u, 2} : Ring{uint32_t(Lay::NKV), uint32_t(Lay::NQ), 1};
+  const Ring ring = plan.splits > 1 ? Ring{uint32_t(Lay::NS), 2} : Ring{uint32_t(Lay::NKV), 1};
 
   // Keys of batch row b that may count (the same row is asked for many times in a row).
   int len_b = -1, len_v = 0;
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sbase + (ring.tile0 + s) * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
+            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
           x ? ++e[1] : ++e[0];
           return true;
         };
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             uint32_t w[4];
             block_words(limit - row, args.mask.keys == nullptr ? nullptr : args.mask.keys + b * args.mask.stride + row,
                         lane, w);
-            zero_rows<D>(sbase + (ring.tile0 + s) * Lay::TILE, w, lane);
+            zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
             __syncwarp();
           }
           if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);
@@ -205,14 +210,47 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             }
         }
       }
+    } else if (warp == 15) {
+      // ============================================================== query loads
+      if (lane == 0) {
+        uint32_t n[2] = {0, 0};
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || it.qt[x] < 0) continue;
+            if (!(ok = cross_wait(&bars[Lay::QE + x], (n[x] & 1) ^ 1, abort_flag, to))) continue;
+            mbar_arrive_expect_tx(&bars[Lay::QF + x], Lay::TILE);
+#pragma unroll
+            for (int c = 0; c < DH; ++c)
+              tma_load_4d(sbase + x * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + x], c * 64, it.qt[x] * 128,
+                          it.h * args.q_h, it.b * args.q_b);
+            ++n[x];
+          }
+          // the next item's into L2: its loads come late, behind this item's last scores
+          if (i + int(gridDim.x) < plan.items) {
+            const CrossItem nx = cross_item(plan, args.heads, i + int(gridDim.x));
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int c = 0; c < DH; ++c)
+                if (nx.qt[x] >= 0)
+                  tma_prefetch_4d(&maps.q, c * 64, nx.qt[x] * 128, nx.h * args.q_h, nx.b * args.q_b);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (n[x]) mbar_wait_drain(&bars[Lay::QF + x], (n[x] - 1) & 1, to);
+      }
     } else if (warp == 13) {
       // ============================================================== MMA issuer
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
       constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
       const uint32_t el = elect_one(), tm = uniform(tmem);
-      const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, 16, 1024),
-                     v0 = sdesc_sw128(sbase + ring.tile0 * Lay::TILE, kCrossBlk, 1024);
+      const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + Lay::KV_OFF, 16, 1024),
+                     v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024);
       auto wait = [&](int bar, uint32_t parity) -> bool {
         return cross_warp_wait(&bars[bar], parity, abort_flag, to);
       };
@@ -225,10 +263,10 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         return at;
       };
       // job x: its pending block (scores issued, P V still to come), that block's value tile and
-      // place in the job; parity of its P V products; jobs begun; parities of its query slots
+      // place in the job; parity of its P V products; jobs begun
       bool pend[2] = {}, pfirst[2] = {}, plast[2] = {}, pnew[2] = {}, pdone[2] = {};
-      uint32_t vpos[2] = {0, 0}, ppar[2] = {0, 0}, jobs[2] = {0, 0}, quse[2] = {0, 0};
-      uint32_t kpos = 0, slot = 0;
+      uint32_t vpos[2] = {0, 0}, ppar[2] = {0, 0}, jobs[2] = {0, 0}, tiles[2] = {0, 0};
+      uint32_t kpos = 0;
       bool ok = true;
       auto step = [&](auto X, bool scores, bool first, bool last, bool two) -> bool {
         constexpr int x = decltype(X)::value;
@@ -255,8 +293,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             vpos[x] = vpos[0];
           }
           if (first) {
-            if (!wait(Lay::QF + slot + x, (quse[x] >> (slot >> 1)) & 1)) return false;
-            quse[x] ^= 1u << (slot >> 1);
+            if (!wait(Lay::QF + x, tiles[x] & 1)) return false;
+            ++tiles[x];
           }
         }
         if (pv) {  // P V of the block before
@@ -275,7 +313,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         // S overwrites the columns that the P V above reads P from: the tensor core runs the
         // products of one thread in issue order
         tc_fence_after();
-        const uint64_t qa = q0 + (slot + x) * (Lay::TILE >> 4), ka = k0 + (kpos & 255u) * (Lay::TILE >> 4);
+        const uint64_t qa = q0 + x * (Lay::TILE >> 4), ka = k0 + (kpos & 255u) * (Lay::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
@@ -283,6 +321,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         }
         tc_commit_by(el, &bars[Lay::SF + x]);
         if (done) tc_commit_by(el, &bars[Lay::KVE + (kpos & 255u)]);
+        if (last) tc_commit_by(el, &bars[Lay::QE + x]);
         pend[x] = true;
         pfirst[x] = first;
         plast[x] = last;
@@ -291,7 +330,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         return true;
       };
 #pragma unroll 1
-      for (int i = blockIdx.x; ok; i += gridDim.x, slot ^= 2u) {
+      for (int i = blockIdx.x; ok; i += gridDim.x) {
         // past the last item: one turn for the products still pending
         const bool more = i < plan.items;
         int nk = 1;
@@ -314,63 +353,31 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     // ================================================================ epilogue
     regs_give<kCrossOtherRegs>();
     const int row = threadIdx.x & 127;
-    uint32_t jobs = 0;              // jobs of each slot so far (a byte each, mod 256)
-    uint32_t qused = 0, qpar = 0;   // per query slot: ever loaded, parity of its loads
+    uint32_t jobs = 0;    // bit x: parity of job slot x's jobs
+    uint32_t halves = 0;  // 64-channel halves staged; half n goes through buffer n & 1
+    const int row0 = (warp & 3) * 32;
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return cross_warp_wait(bar, parity, abort_flag, to);
     };
-    // the query tile of job x of item i into slot s, where there is such a job
-    auto load_q = [&](long long i, int x, uint32_t s) {
-      if (i >= plan.items) return;
-      const CrossItem it = cross_item(plan, args.heads, int(i));
-      const int qt = x ? it.qt[1] : it.qt[0];
-      if (qt < 0) return;
-      mbar_arrive_expect_tx(&bars[Lay::QF + s], Lay::TILE);
-#pragma unroll
-      for (int c = 0; c < DH; ++c)
-        tma_load_4d(sbase + s * Lay::TILE + c * kCrossBlk, &maps.q, &bars[Lay::QF + s], c * 64, qt * 128,
-                    it.h * args.q_h, it.b * args.q_b);
-      qused |= 1u << s;
-      qpar ^= 1u << s;
-    };
-    if (threadIdx.x == 256) {
 #pragma unroll 1
-      for (int s = 0; s < 4; ++s) load_q((long long)blockIdx.x + (s >> 1) * (long long)gridDim.x, s & 1, s);
-    }
-    __syncwarp();
-    uint32_t item = 0;
-#pragma unroll 1
-    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
+    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
 #pragma unroll 1
       for (int x = 0; ok && x < 2; ++x) {
-        const uint32_t s = 2 * (item & 1) + x;
         const int qt = x ? it.qt[1] : it.qt[0];
-        if (qt < 0) {
-          if (threadIdx.x == 256) load_q(i + 2ll * gridDim.x, x, s);
-          __syncwarp();
-          continue;
-        }
-        const uint32_t job = (jobs >> (8 * x)) & 255u;
-        jobs = x ? (jobs & 0xffu) | ((job + 1) & 255u) << 8 : (jobs & 0xff00u) | ((job + 1) & 255u);
-        // two barriers in turn: the softmax may finish the next job before this wait begins
-        if (!(ok = wwait(&bars[Lay::LF + 2 * x + (job & 1)], (job >> 1) & 1))) break;
-        const uint32_t tile = sbase + s * Lay::TILE;
+        if (qt < 0) continue;
+        const uint32_t job = (jobs >> x) & 1u;
+        jobs ^= 1u << x;
+        if (!(ok = wwait(&bars[Lay::LF + x], job))) break;
         float m2, l;  // maximum (base 2) and sum of the row
-        ld_shared_f2(tile + (row >> 5) * 4096 + lane * 8, m2, l);
+        ld_shared_f2(sbase + Lay::STAT_OFF + (x * 128 + row) * 8, m2, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Lay::LE + x]);
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
         const int tok = qt * 128 + row;
-        if (tok < args.n) {
-          const float l2 = l == 0.f ? -INFINITY : m2 + log2f(l);
-          const long long r = ((long long)it.b * args.heads + it.h) * args.n + tok;
-          if (plan.splits > 1)
-            args.part_lse[(long long)(it.sp[0] + x) * args.B * args.heads * args.n + r] = l2;
-          else if (args.lse != nullptr)
-            args.lse[r] = l2 * 0.69314718055994530942f;
-        }
-        __syncwarp();  // the statistics are read before the rows of this warp are staged over them
-        if (!(ok = wwait(&bars[Lay::OF + x], job & 1))) break;
+        __syncwarp();
+        if (!(ok = wwait(&bars[Lay::OF + x], job))) break;
         tc_fence_after();
         const uint32_t t = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
         if (plan.splits > 1) {
@@ -390,62 +397,53 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
               }
             }
           }
+          if (tok < args.n)
+            args.part_lse[(long long)(it.sp[0] + x) * args.B * args.heads * args.n +
+                          ((long long)it.b * args.heads + it.h) * args.n + tok] = l == 0.f ? -INFINITY : m2 + log2f(l);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars[Lay::ST + x]);
-            mbar_arrive(&bars[Lay::OE + x]);
-          }
-          // the statistics of every warp's rows are read before the next query tile comes
-          if (threadIdx.x == 256) {
-            ok = cross_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
-            if (ok) load_q(i + 2ll * gridDim.x, x, s);
-          }
-          ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+          if (lane == 0) mbar_arrive(&bars[Lay::OE + x]);
           continue;
         }
-        const uint32_t stage = tile + row * 128;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(t + c, v);
-          // 1 / sum is 0 for a row without keys; what the products hold there is not looked at
+        for (int h = 0; h < DH; ++h, ++halves) {
+          const uint32_t stage = sbase + Lay::STAGE_OFF + (halves & 1) * kCrossBlk + row0 * 128;
+          // the store before the last has read this buffer
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(t + 64 * h + c, v);
+            // 1 / sum is 0 for a row without keys; what the products hold there is not looked at
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t p[4];
+            for (int j = 0; j < 4; ++j) {
+              uint32_t p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = inv == 0.f ? 0u
-                                : pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * inv,
-                                              __uint_as_float(v[8 * j + 2 * e + 1]) * inv);
-            const int chunk = ((c & 32) >> 3) + j;
-            st_shared_v4(stage + (c >> 6) * kCrossBlk + ((chunk ^ (row & 7)) << 4), p[0], p[1], p[2], p[3]);
+              for (int e = 0; e < 4; ++e)
+                p[e] = inv == 0.f ? 0u
+                                  : pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * inv,
+                                                __uint_as_float(v[8 * j + 2 * e + 1]) * inv);
+              st_shared_v4(stage + lane * 128 + ((((c >> 3) + j) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+            }
+          }
+          tc_fence_before();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (h == DH - 1) mbar_arrive(&bars[Lay::OE + x]);  // O is read
+            if (qt * 128 + row0 < args.n)
+              tma_store_4d(&maps.o, stage, h * 64, qt * 128 + row0, it.h * args.o_h, it.b * args.o_b);
+            bulk_commit();
           }
         }
-        tc_fence_before();
-        fence_async_smem();
-        __syncwarp();
-        // ST before OE: the next job of this slot, and so the next arrivals at its ST, wait for OE,
-        // so no warp can arrive for it while another has yet to arrive for this job
-        if (lane == 0) {
-          mbar_arrive(&bars[Lay::ST + x]);
-          mbar_arrive(&bars[Lay::OE + x]);
-        }
-        if (threadIdx.x == 256) {  // stores the tile once all four warps have staged their rows
-          ok = cross_wait(&bars[Lay::ST + x], job & 1, abort_flag, to);
-#pragma unroll
-          for (int c = 0; ok && c < DH; ++c)
-            tma_store_4d(&maps.o, tile + c * kCrossBlk, c * 64, qt * 128, it.h * args.o_h, it.b * args.o_b);
-          bulk_commit();
-          bulk_wait_read();
-          if (ok) load_q(i + 2ll * gridDim.x, x, s);
-        }
-        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        // behind the staging, whose fence would wait for it
+        if (args.lse != nullptr && tok < args.n)
+          args.lse[((long long)it.b * args.heads + it.h) * args.n + tok] =
+              l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994530942f;
       }
     }
-    if (threadIdx.x == 256)
-      for (int s = 0; s < 4; ++s)
-        if ((qused >> s) & 1u) mbar_wait_drain(&bars[Lay::QF + s], ((qpar >> s) & 1u) ^ 1u, to);
+    if (lane == 0) bulk_wait_read();
   } else {
     // ================================================================ softmax
     regs_take<kCrossSoftmaxRegs>();
@@ -454,13 +452,12 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     const uint32_t tO = tmem + (uint32_t((warp & 3) * 32) << 16) + 256 + D * x;
     const float c2 = args.scale_log2;
     const uint64_t c2x2 = f2(c2, c2);
-    uint32_t sc = 0, jobs = 0;
+    uint32_t sc = 0, jobs = 0;  // blocks and jobs so far
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return cross_warp_wait(bar, parity, abort_flag, to);
     };
-    uint32_t item = 0;
-    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x, ++item) {
+    for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
       const int qt = x ? it.qt[1] : it.qt[0];
       if (qt < 0) continue;
@@ -564,10 +561,11 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         m_run = m_use;
       }
       if (!ok) break;
-      // the row's statistics for the epilogue, in the query tile that no product reads any more
-      st_shared_f2(sbase + (2 * (item & 1) + x) * Lay::TILE + (row >> 5) * 4096 + lane * 8, m_run * c2, l_run);
+      // the row's statistics for the epilogue, which has read the last job's
+      if (!(ok = wwait(&bars[Lay::LE + x], (jobs & 1) ^ 1))) break;
+      st_shared_f2(sbase + Lay::STAT_OFF + (x * 128 + row) * 8, m_run * c2, l_run);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Lay::LF + 2 * x + (jobs & 1)]);
+      if (lane == 0) mbar_arrive(&bars[Lay::LF + x]);
       ++jobs;
     }
   }
