@@ -334,18 +334,19 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   if ((s = encode_rows(&maps.k, dev, c.k, d->k, B, hk, d->m, D, &a.k_b, &a.k_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.v, dev, c.v, d->v, B, hk, d->m, D, &a.v_b, &a.v_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.dout, dev, c.dout, d->dout, B, h, d->n, D, &a.do_b, &a.do_h)) != SQUAD_OK) return s;
-  if ((s = encode_rows(&maps.dq, dev, c.dq, d->dq, B, h, d->n, D, &a.dq_b, &a.dq_h)) != SQUAD_OK) return s;
-  a.mask = c.mask;
+a.mask = c.mask;
   a.scale = c.scale;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.o = static_cast<const __nv_bfloat16*>(c.o_in);
   a.dout = static_cast<const __nv_bfloat16*>(c.dout);
   a.so = c.so;
   a.sdo = c.sdo;
+  a.sdq = c.sdq;
   a.sdk = c.sdk;
   a.sdv = c.sdv;
   a.lse = c.lse;
   a.Drow = c.Drow;
+  a.dq = static_cast<__nv_bfloat16*>(c.dq);
   a.dk = static_cast<__nv_bfloat16*>(c.dk);
   a.dv = static_cast<__nv_bfloat16*>(c.dv);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);

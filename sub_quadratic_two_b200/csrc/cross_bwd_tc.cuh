@@ -21,7 +21,7 @@ namespace sq {
 constexpr int kCrossBwdThreads = 512;
 
 struct alignas(64) CrossBwdMaps {
-  CUtensorMap q, k, v, dout, dq;
+  CUtensorMap q, k, v, dout;
 };
 
 struct CrossBwdArgs {
@@ -30,14 +30,14 @@ struct CrossBwdArgs {
   int splits;             // dk, dv kernel: parts of a key tile's queries
   int items;              // dq kernel: query tiles in all; dk, dv kernel: (key tile, split) units
   FastDiv f_qtiles, f_heads, f_group, f_kblocks, f_kv_heads;
-  int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h, dq_b, dq_h;  // 1, or 0 where the map has no such extent
+  int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h;  // 1, or 0 where the map has no such extent
   CrossMask mask;
   float scale, scale_log2;
   const __nv_bfloat16 *o, *dout;  // for D
-  CrossStride so, sdo, sdk, sdv;
+  CrossStride so, sdo, sdq, sdk, sdv;
   const float* lse;       // [B, heads, n]
   float* Drow;            // [B, heads, n]: written by the dq kernel, read by the other
-  __nv_bfloat16 *dk, *dv;
+  __nv_bfloat16 *dq, *dk, *dv;
   float* part;            // splits > 1: [dk, dv][split][B, kv_heads, kblocks * 128][D] fp32
   int* err;
   uint64_t timeout_ns;
@@ -47,11 +47,12 @@ struct CrossBwdArgs {
 //
 // Roles (512 threads):
 //   warps 0-3, 4-7  key columns 0-63 and 64-127 of each block (thread = query row = TMEM lane)
-//   warps 8-11      D of the next tile (from dO and O in memory), then dQ of this one:
-//                   TMEM -> bf16 -> the Q tile in shared memory -> TMA store; their first thread
-//                   then loads the query tile after next into that place
-//   warp 12         key tiles;  warp 15: value tiles and dO;  warp 13: tcgen05.mma
+//   warps 8-11      D of the next tile (from dO and O in memory), then dQ of this one: TMEM -> bf16
+//                   rows, 64 bytes of a row per thread and step (there is no room to stage them)
+//   warp 12         key tiles and Q;  warp 15: value tiles and dO;  warp 13: tcgen05.mma
 //   warp 14         zeroes masked rows of key and value tiles
+// Where all keys that may count lie in one block, D = sum_j P dP is summed by warps 0-7 instead: it
+// costs no read of O, and it is free of O's rounding, which few keys do not average out.
 // TMEM: S of block t at [128 (t & 1), ...), dP at [256, 384), dQ at [384, 384 + D). dS replaces
 // S in place (packed bf16, each half inside its own columns).
 // Per block the tensor core runs S(t+1), dP(t+1), dQ(t); the exponentials of block t+1 run
@@ -60,16 +61,17 @@ struct CrossBwdArgs {
 template <int D>
 struct CrossDqLayout {
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4, NDO = D == 128 ? 1 : 2;
+  // A key tile stays from S(t) to dQ(t): with two, S(t + 1) waits for dQ(t - 1) and a load.
+  static constexpr int NK = D == 128 ? 3 : 4, NV = D == 128 ? 2 : 4;
   static constexpr int Q_OFF = 0;
-  static constexpr int DO_OFF = 2 * TILE;
-  static constexpr int K_OFF = DO_OFF + NDO * TILE;
+  static constexpr int DO_OFF = TILE;
+  static constexpr int K_OFF = DO_OFF + TILE;
   static constexpr int V_OFF = K_OFF + NK * TILE;
-  static constexpr int D_OFF = V_OFF + NV * TILE;  // D of two tiles
-  static constexpr int BAR_OFF = D_OFF + 2 * 128 * 4;
-  static constexpr int QF = 0, DOF = QF + 2, DOE = DOF + NDO, KF = DOE + NDO, KE = KF + NK, KR = KE + NK, VF = KR + NK,
-                       VE = VF + NV, VR = VE + NV, SF = VR + NV, DPF = SF + 2, DSF = DPF + 1, OF = DSF + 1, OE = OF + 1,
-                       DF = OE + 1, DE = DF + 2, ST = DE + 2, DRAIN = ST + 1, NBAR = DRAIN + 1;
+  static constexpr int D_OFF = V_OFF + NV * TILE;  // half sums of D, two tiles in turn
+  static constexpr int BAR_OFF = D_OFF + 4 * 128 * 4;
+  static constexpr int QF = 0, QE = 1, DOF = 2, DOE = 3, KF = 4, KE = KF + NK, KR = KE + NK, VF = KR + NK, VE = VF + NV,
+                       VR = VE + NV, SF = VR + NV, DPF = SF + 2, DSF = DPF + 1, OF = DSF + 1, OE = OF + 1, DF = OE + 1,
+                       DE = DF + 2, XD = DE + 2, DRAIN = XD + 4, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR_OFF + Lay::NBAR * 8 + 4);
-  float* d_smem = reinterpret_cast<float*>(smem + Lay::D_OFF);
+  float* half_sum = reinterpret_cast<float*>(smem + Lay::D_OFF);  // [parity][half][row]
   const int warp = int(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint64_t to = args.timeout_ns;
   if (smem_u32(smem) & 1023u) {
@@ -92,8 +94,8 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::NBAR; ++i) {
-      const int warps = i == Lay::DSF ? 8 : i >= Lay::DE && i < Lay::DE + 2 ? 8 : i == Lay::OE || i == Lay::ST ? 4
-                        : i >= Lay::DF && i < Lay::DF + 2 ? 4 : 1;
+      const int warps = i == Lay::DSF || (i >= Lay::DE && i < Lay::DE + 2) ? 8
+                        : i == Lay::OE || (i >= Lay::DF && i < Lay::DF + 2) ? 4 : i >= Lay::XD && i < Lay::XD + 4 ? 2 : 1;
       mbar_init(&bars[i], warps);
     }
     *abort_flag = 0;
@@ -108,7 +110,6 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
     prefetch_tmap(&maps.dout);
-    prefetch_tmap(&maps.dq);
   }
   tc_fence_before();
   __syncthreads();
@@ -151,20 +152,35 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   };
 
   if (warp == 12) {
-    if (lane == 0) {  // ---------------------------------------------- key tiles
-      uint32_t e = 0;
+    if (lane == 0) {  // ---------------------------------------------- key tiles and Q
+      uint32_t e = 0, q = 0;
       bool ok = true;
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         const Item it = item_of(i);
         const int nk = blocks_of(it.b);
+        // the next tile's Q and dO into L2: their loads come late, behind this tile's last products
+        if (i + int(gridDim.x) < args.items) {
+          const Item nx = item_of(i + int(gridDim.x));
+#pragma unroll
+          for (int c = 0; c < DH; ++c) {
+            tma_prefetch_4d(&maps.q, c * 64, nx.qt * 128, nx.h * args.q_h, nx.b * args.q_b);
+            tma_prefetch_4d(&maps.dout, c * 64, nx.qt * 128, nx.h * args.do_h, nx.b * args.do_b);
+          }
+        }
         for (int k = 0; ok && k < nk; ++k) {
           const uint32_t s = e % Lay::NK;
           if (!(ok = cross_wait(&bars[Lay::KE + s], ((e / Lay::NK) & 1) ^ 1, abort_flag, to))) break;
           load(sbase + Lay::K_OFF + s * Lay::TILE, &maps.k, &bars[Lay::KF + s], k * 128, it.hk * args.k_h, it.b * args.k_b);
           ++e;
+          if (k == 0) {
+            if (!(ok = cross_wait(&bars[Lay::QE], (q & 1) ^ 1, abort_flag, to))) break;
+            load(sbase + Lay::Q_OFF, &maps.q, &bars[Lay::QF], it.qt * 128, it.h * args.q_h, it.b * args.q_b);
+            ++q;
+          }
         }
       }
       drain_ring(Lay::KF, Lay::NK, e);
+      drain_ring(Lay::QF, 1, q);
     }
   } else if (warp == 15) {
     if (lane == 0) {  // ---------------------------------------------- value tiles and dO
@@ -179,16 +195,14 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
           load(sbase + Lay::V_OFF + s * Lay::TILE, &maps.v, &bars[Lay::VF + s], k * 128, it.hk * args.v_h, it.b * args.v_b);
           ++e;
           if (k == 0) {
-            const uint32_t z = q % Lay::NDO;
-            if (!(ok = cross_wait(&bars[Lay::DOE + z], ((q / Lay::NDO) & 1) ^ 1, abort_flag, to))) break;
-            load(sbase + Lay::DO_OFF + z * Lay::TILE, &maps.dout, &bars[Lay::DOF + z], it.qt * 128, it.h * args.do_h,
-                 it.b * args.do_b);
+            if (!(ok = cross_wait(&bars[Lay::DOE], (q & 1) ^ 1, abort_flag, to))) break;
+            load(sbase + Lay::DO_OFF, &maps.dout, &bars[Lay::DOF], it.qt * 128, it.h * args.do_h, it.b * args.do_b);
             ++q;
           }
         }
       }
       drain_ring(Lay::VF, Lay::NV, e);
-      drain_ring(Lay::DOF, Lay::NDO, q);
+      drain_ring(Lay::DOF, 1, q);
     }
   } else if (warp == 14) {
     if (MASKED) {  // ------------------------------------------------- masked rows to zero
@@ -245,23 +259,22 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
       const Item it = item_of(i);
       const int nk = int(uniform(uint32_t(blocks_of(it.b))));
-      const uint32_t z = job % Lay::NDO;
-      const uint64_t qa = q0 + (job & 1) * (Lay::TILE >> 4), da = o0 + z * (Lay::TILE >> 4);
 #pragma unroll 1
       for (int k = 0; k < nk; ++k, ++t) {
         const bool first = k == 0, last = k == nk - 1;
         const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
         // S(t) into the columns that dQ(t - 2) read dS from (issued before, so behind it)
         if (!(ok = wait(KREADY + sk, (t / Lay::NK) & 1))) break;
-        if (first && !(ok = wait(Lay::QF + (job & 1), (job >> 1) & 1))) break;
+        if (first && !(ok = wait(Lay::QF, job & 1))) break;
         tc_fence_after();
         const uint64_t ka = k0 + sk * (Lay::TILE >> 4), va = v0 + sv * (Lay::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
-          mma_ss_by(el, tm + 128 * (t & 1), qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
+          mma_ss_by(el, tm + 128 * (t & 1), q0 + off, ka + off, id_s, kk > 0 ? 1u : 0u);
         }
         tc_commit_by(el, &bars[Lay::SF + (t & 1)]);
+        if (last) tc_commit_by(el, &bars[Lay::QE]);
         // dS(t - 1) is written, so dP(t - 1) has been read. At a new tile dO has yet to arrive: dQ
         // of the last block goes first. Else the value tile is waited for ahead of dS.
         if (!first && !(ok = wait(VREADY + sv, (t / Lay::NV) & 1))) break;
@@ -269,17 +282,17 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         if (first) {
           if (prev && !(ok = dq(t - 1, job - 1, prev_first, prev_last))) break;
           if (!(ok = wait(VREADY + sv, (t / Lay::NV) & 1))) break;
-          if (!(ok = wait(Lay::DOF + z, (job / Lay::NDO) & 1))) break;
+          if (!(ok = wait(Lay::DOF, job & 1))) break;
         }
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
-          mma_ss_by(el, tm + 256, da + off, va + off, id_s, kk > 0 ? 1u : 0u);
+          mma_ss_by(el, tm + 256, o0 + off, va + off, id_s, kk > 0 ? 1u : 0u);
         }
         tc_commit_by(el, &bars[Lay::DPF]);
         tc_commit_by(el, &bars[Lay::VE + sv]);
-        if (last) tc_commit_by(el, &bars[Lay::DOE + z]);
+        if (last) tc_commit_by(el, &bars[Lay::DOE]);
         if (!first && !(ok = dq(t - 1, job, prev_first, prev_last))) break;
         prev = true;
         prev_first = first;
@@ -326,10 +339,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
 #pragma unroll
           for (int z = LPR / 2; z > 0; z >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, z);
           const int tok = r0 + (g + u) * RPI;
-          if (lane % LPR == 0) {
-            d_smem[par * 128 + tok - it.qt * 128] = acc;
-            if (tok < args.n) args.Drow[base + tok] = acc;
-          }
+          if (lane % LPR == 0 && tok < args.n) args.Drow[base + tok] = acc;
         }
       }
       __syncwarp();
@@ -337,72 +347,50 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       ++made;
       return true;
     };
-    auto load_q = [&](int i, uint32_t job) {
-      const Item it = item_of(i);
-      load(sbase + Lay::Q_OFF + (job & 1) * Lay::TILE, &maps.q, &bars[Lay::QF + (job & 1)], it.qt * 128,
-           it.h * args.q_h, it.b * args.q_b);
+    // D of the tiles whose keys span several blocks (the others' comes with their dS)
+    auto make_d_if = [&](int i) -> bool {
+      return i >= args.items || blocks_of(item_of(i).b) == 1 || make_d(i);
     };
-    uint32_t qloads = 0;
-    if (threadIdx.x == 256) {
-      for (int i = blockIdx.x; qloads < 2 && i < args.items; i += gridDim.x, ++qloads) load_q(i, qloads);
-    }
-    __syncwarp();
-    if (int(blockIdx.x) < args.items) ok = make_d(blockIdx.x);
+    ok = make_d_if(blockIdx.x);
     uint32_t job = 0;
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
-      if (i + int(gridDim.x) < args.items && !(ok = make_d(i + gridDim.x))) break;
+      if (!(ok = make_d_if(i + int(gridDim.x)))) break;
       const Item it = item_of(i);
       if (!(ok = cross_warp_wait(&bars[Lay::OF], job & 1, abort_flag, to))) break;
       tc_fence_after();
       const uint32_t t = tmem + (uint32_t(ew * 32) << 16) + 384;
-      const uint32_t tile = sbase + Lay::Q_OFF + (job & 1) * Lay::TILE, stage = tile + row * 128;
+      const int tok = it.qt * 128 + row;
+      __nv_bfloat16* out = args.dq + it.b * args.sdq.b + it.h * args.sdq.h + (long long)tok * args.sdq.n;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
+        __syncwarp();  // lanes part below: TMEM is read by whole warps
         tmem_ld32(t + c, v);
+        if (tok < args.n) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t p[4];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * args.scale,
-                               __uint_as_float(v[8 * j + 2 * e + 1]) * args.scale);
-          const int chunk = ((c & 32) >> 3) + j;
-          st_shared_v4(stage + (c >> 6) * kCrossBlk + ((chunk ^ (row & 7)) << 4), p[0], p[1], p[2], p[3]);
+            for (int e = 0; e < 4; ++e)
+              p[e] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * args.scale,
+                                 __uint_as_float(v[8 * j + 2 * e + 1]) * args.scale);
+            *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
         }
       }
       tc_fence_before();
-      fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars[Lay::ST]);  // before OE, which the next tile's arrivals at ST wait for
-        mbar_arrive(&bars[Lay::OE]);
-      }
-      if (threadIdx.x == 256) {
-        ok = cross_wait(&bars[Lay::ST], job & 1, abort_flag, to);
-#pragma unroll
-        for (int c = 0; ok && c < DH; ++c)
-          tma_store_4d(&maps.dq, tile + c * kCrossBlk, c * 64, it.qt * 128, it.h * args.dq_h, it.b * args.dq_b);
-        bulk_commit();
-        bulk_wait_read();
-        const long long next = (long long)i + 2ll * gridDim.x;
-        if (ok && next < args.items) {
-          load_q(int(next), job);
-          ++qloads;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      if (lane == 0) mbar_arrive(&bars[Lay::OE]);
     }
-    if (threadIdx.x == 256) drain_ring(Lay::QF, 2, qloads);
   } else {
     // ------------------------------------------------------------------ P, dS
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const float c2 = args.scale_log2;
     const uint64_t c2x2 = f2(c2, c2);
-    uint32_t t = 0, job = 0;
+    uint32_t t = 0, made = 0, summed = 0;  // blocks; tiles with D from the epilogue, and summed here
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
+    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
       const Item it = item_of(i);
       const int len = len_of(it.b), nk = blocks_of(it.b), tok = it.qt * 128 + row;
       const bool idle = it.qt * 128 + (warp & 3) * 32 >= args.n;
@@ -454,14 +442,40 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
             }
           }
         }
-        if (k == 0) {
-          if (!(ok = cross_warp_wait(&bars[Lay::DF + (job & 1)], (job >> 1) & 1, abort_flag, to))) break;
-          Dv = d_smem[(job & 1) * 128 + row];
+        if (k == 0 && nk > 1) {
+          if (!(ok = cross_warp_wait(&bars[Lay::DF + (made & 1)], (made >> 1) & 1, abort_flag, to))) break;
+          // written by this CTA's epilogue warps, ordered by the barrier (so not read as constant data)
+          if (tok < args.n) Dv = *static_cast<volatile float*>(args.Drow + ((long long)it.b * args.heads + it.h) * args.n + tok);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[Lay::DE + (job & 1)]);
+          if (lane == 0) mbar_arrive(&bars[Lay::DE + (made & 1)]);
+          ++made;
         }
         if (!(ok = cross_warp_wait(&bars[Lay::DPF], t & 1, abort_flag, to))) break;
         tc_fence_after();
+        if (nk == 1 && !idle) {
+          // D of the row: each half's sum of P dP, exchanged with the warp of the other half
+          uint64_t acc = 0ull;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[16];
+            tmem_ld16_async(tP + 16 * c, u);
+            tmem_ld_wait(u);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              acc = ffma2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), f2(p[16 * c + e], p[16 * c + e + 1]), acc);
+          }
+          float* hs = half_sum + (summed & 1) * 256;
+          Dv = f2_lo(acc) + f2_hi(acc);
+          hs[g * 128 + row] = Dv;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Lay::XD + (warp & 3)]);
+          if (!(ok = cross_warp_wait(&bars[Lay::XD + (warp & 3)], summed & 1, abort_flag, to))) break;
+          // the same sum on both sides
+          const float other = hs[(g ^ 1) * 128 + row];
+          Dv = g ? other + Dv : Dv + other;
+          if (g == 0 && tok < args.n) args.Drow[((long long)it.b * args.heads + it.h) * args.n + tok] = Dv;
+          ++summed;
+        }
         if (!idle) {
           const uint64_t nd = f2(-Dv, -Dv);
           uint32_t v[2][16];
