@@ -204,11 +204,11 @@ FwdWs fwd_workspace(const squad_cross_desc* d) {
   return w;
 }
 
-template <int D, bool MASKED>
+template <int D, int MASK>
 squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& maps, const sq::CrossFwdArgs& a,
                               cudaStream_t st) {
   using Lay = sq::CrossFwdLayout<D>;
-  auto kern = sq::cross_fwd_tc_kernel<D, MASKED>;
+  auto kern = sq::cross_fwd_tc_kernel<D, MASK>;
   static std::atomic<bool> done[kMaxDevices];
   squad_status s = allow_smem(kern, Lay::BYTES, dev, done);
   if (s != SQUAD_OK) return s;
@@ -242,11 +242,15 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
     a.part_o = static_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part_lse);
   }
-  const bool masked = c.mask.lens != nullptr || c.mask.keys != nullptr;
+  const int mask = c.mask.keys != nullptr ? 2 : c.mask.lens != nullptr ? 1 : 0;
   if (d->d == 128)
-    s = masked ? launch_cross_fwd<128, true>(dev, maps, a, st) : launch_cross_fwd<128, false>(dev, maps, a, st);
+    s = mask == 2   ? launch_cross_fwd<128, 2>(dev, maps, a, st)
+        : mask == 1 ? launch_cross_fwd<128, 1>(dev, maps, a, st)
+                    : launch_cross_fwd<128, 0>(dev, maps, a, st);
   else
-    s = masked ? launch_cross_fwd<64, true>(dev, maps, a, st) : launch_cross_fwd<64, false>(dev, maps, a, st);
+    s = mask == 2   ? launch_cross_fwd<64, 2>(dev, maps, a, st)
+        : mask == 1 ? launch_cross_fwd<64, 1>(dev, maps, a, st)
+                    : launch_cross_fwd<64, 0>(dev, maps, a, st);
   if (s != SQUAD_OK || a.plan.splits <= 1) return s;
   const long long rows = (long long)d->B * d->heads * d->n;
   const unsigned blocks = unsigned((rows + 3) / 4);

@@ -50,7 +50,8 @@ struct CrossBwdArgs {
 //   warps 8-11      D of the next tile (from dO and O in memory), then dQ of this one: TMEM -> bf16
 //                   rows, 64 bytes of a row per thread and step (there is no room to stage them)
 //   warp 12         key tiles and Q;  warp 15: value tiles and dO;  warp 13: tcgen05.mma
-//   warp 14         zeroes masked rows of key and value tiles
+//   warp 14         masks: which keys of a block count, for warps 0-7, and zeroes in the masked rows of
+//                   key and value tiles
 // Where all keys that may count lie in one block, D = sum_j P dP is summed by warps 0-7 instead: it
 // costs no read of O, and it is free of O's rounding, which few keys do not average out.
 // TMEM: S of block t at [128 (t & 1), ...), dP at [256, 384), dQ at [384, 384 + D). dS replaces
@@ -68,10 +69,12 @@ struct CrossDqLayout {
   static constexpr int K_OFF = DO_OFF + TILE;
   static constexpr int V_OFF = K_OFF + NK * TILE;
   static constexpr int D_OFF = V_OFF + NV * TILE;  // half sums of D, two tiles in turn
-  static constexpr int BAR_OFF = D_OFF + 4 * 128 * 4;
+  static constexpr int NW = 8;                     // blocks whose masks are kept
+  static constexpr int WORD_OFF = D_OFF + 4 * 128 * 4;
+  static constexpr int BAR_OFF = WORD_OFF + NW * 16;
   static constexpr int QF = 0, QE = 1, DOF = 2, DOE = 3, KF = 4, KE = KF + NK, KR = KE + NK, VF = KR + NK, VE = VF + NV,
                        VR = VE + NV, SF = VR + NV, DPF = SF + 2, DSF = DPF + 1, OF = DSF + 1, OE = OF + 1, DF = OE + 1,
-                       DE = DF + 2, XD = DE + 2, DRAIN = XD + 4, NBAR = DRAIN + 1;
+                       DE = DF + 2, XD = DE + 2, WF = XD + 4, DRAIN = WF + NW, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       drain_ring(Lay::DOF, 1, q);
     }
   } else if (warp == 14) {
-    if (MASKED) {  // ------------------------------------------------- masked rows to zero
+    if (MASKED) {  // ------------------------------------------------- masks
       uint32_t t = 0;
       bool ok = true;
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
@@ -219,7 +222,14 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
           if (!(ok = cross_warp_wait(&bars[Lay::KF + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
           zero_rows<D>(sbase + Lay::K_OFF + sk * Lay::TILE, w, lane);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[Lay::KR + sk]);
+          // the block's place is free: K(t) came behind dQ(t - NK), whose dS is written (NK < NW)
+          if (lane == 0) {
+            if (args.mask.keys != nullptr) {
+              st_shared_v4(sbase + Lay::WORD_OFF + (t % Lay::NW) * 16, w[0], w[1], w[2], w[3]);
+              mbar_arrive(&bars[Lay::WF + t % Lay::NW]);
+            }
+            mbar_arrive(&bars[Lay::KR + sk]);
+          }
           if (!(ok = cross_warp_wait(&bars[Lay::VF + sv], (t / Lay::NV) & 1, abort_flag, to))) break;
           zero_rows<D>(sbase + Lay::V_OFF + sv * Lay::TILE, w, lane);
           __syncwarp();
@@ -403,43 +413,36 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       const uint64_t neg2 = f2(-lse2, -lse2);
       float Dv = 0.f;
       for (int k = 0; k < nk; ++k, ++t) {
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-        const unsigned char* keys =
-            !MASKED || args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + k * 128;
-        if (len - k * 128 < 128 || keys != nullptr) block_words(len - k * 128, keys, lane, w);
-        const uint32_t wa = g ? w[2] : w[0], wb = g ? w[3] : w[1];
         const uint32_t tS = tmem + lanes + 128 * (t & 1) + 64 * g, tP = tmem + lanes + 256 + 64 * g;
         if (!(ok = cross_warp_wait(&bars[Lay::SF + (t & 1)], (t >> 1) & 1, abort_flag, to))) break;
         tc_fence_after();
-        // a block that does not count whole: its masked scores become -inf where they lie
-        if ((wa & wb) != ~0u && !idle) {
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t word = c ? wb : wa;
-            uint32_t v[32];
-            tmem_ld32(tS + 32 * c, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((word >> e) & 1u)) v[e] = 0xff800000u;
-            tmem_st32(tS + 32 * c, v);
-          }
-          tmem_st_wait();
+        // which of this half's keys count
+        uint32_t wa, wb;
+        if (MASKED && args.mask.keys != nullptr) {
+          if (!(ok = cross_warp_wait(&bars[Lay::WF + t % Lay::NW], (t / Lay::NW) & 1, abort_flag, to))) break;
+          const uint4 w = ld_shared_v4(sbase + Lay::WORD_OFF + (t % Lay::NW) * 16);
+          wa = g ? w.z : w.x;
+          wb = g ? w.w : w.y;
+        } else {
+          uint32_t w[4];
+          block_words(len - k * 128, nullptr, lane, w);
+          wa = g ? w[2] : w[0];
+          wb = g ? w[3] : w[1];
         }
         float p[64];
         if (!idle) {
-          uint32_t v[2][16];
-          tmem_ld16_async(tS, v[0]);
+          uint32_t v[64];
+          tmem_ld64(tS, v);
+          if ((wa & wb) != ~0u) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&u)[16] = v[c & 1];
-            tmem_ld_wait(u);
-            if (c < 3) tmem_ld16_async(tS + 16 * (c + 1), v[(c + 1) & 1]);
+            for (int e = 0; e < 64; ++e)
+              if (!(((e < 32 ? wa : wb) >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+          }
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const uint64_t z = ffma2(f2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), c2x2, neg2);
-              p[16 * c + e] = ex2_approx(f2_lo(z));
-              p[16 * c + e + 1] = ex2_approx(f2_hi(z));
-            }
+          for (int e = 0; e < 64; e += 2) {
+            const uint64_t z = ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg2);
+            p[e] = ex2_approx(f2_lo(z));
+            p[e + 1] = ex2_approx(f2_hi(z));
           }
         }
         if (k == 0 && nk > 1) {

@@ -13,8 +13,9 @@
 //                   each job where the keys are split)
 //   warp 15         TMA loads of query tiles: the next item's as soon as a job's last scores are made
 //   warp 13         issues every tcgen05.mma (the whole warp runs the loop, one lane's count)
-//   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies
-//                   there may be NaN or infinite, and P = 0 times NaN is NaN)
+//   warp 14         masks: tells the softmax warps which keys of a block count, and zeroes the masked
+//                   rows of value tiles before they are used (what lies there may be NaN or
+//                   infinite, and P = 0 times NaN is NaN)
 // TMEM (512 columns): S of job x at [128x, 128x+128), O at [256 + D x, ...). P overwrites S in
 // place as packed bf16.
 // The order of the products is S0(0) S1(0) | PV0(0) S0(1) | PV1(0) S1(1) | ...: the jobs take
@@ -36,6 +37,7 @@
 namespace sq {
 
 constexpr int kCrossThreads = 512;
+constexpr int kCrossWords = 8;  // blocks whose masks are kept
 // Registers per thread: the eight softmax warps hold a whole row of scores (128), the others
 // need few. 256 * 184 + 256 * 72 = 512 * 128, the block's share at launch.
 constexpr int kCrossSoftmaxRegs = 184, kCrossOtherRegs = 72;
@@ -70,18 +72,22 @@ struct CrossFwdLayout {
   // needs every phase.)
   static constexpr int NS = NKV / 2;
   static constexpr int STAT_OFF = KV_OFF + NKV * TILE;   // (maximum, sum) of each job's rows
-  static constexpr int BAR_OFF = STAT_OFF + 2 * 128 * 8;
+  static constexpr int WORD_OFF = STAT_OFF + 2 * 128 * 8;  // masks of eight blocks of each ring
+  static constexpr int BAR_OFF = WORD_OFF + 2 * kCrossWords * 16;
   static constexpr int QF = 0, QE = QF + 2, KVF = QE + 2, KVE = KVF + NKV, RDY = KVE + NKV, SF = RDY + NKV, PF = SF + 2,
-                       OF = PF + 2, OE = OF + 2, LF = OE + 2, LE = LF + 2, DRAIN = LE + 2, NBAR = DRAIN + 1;
+                       OF = PF + 2, OE = OF + 2, LF = OE + 2, LE = LF + 2, WF = LE + 2, DRAIN = WF + 2 * kCrossWords, NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
-template <int D, bool MASKED>
+// MASK: which keys count is bounded by 0: m alone, 1: a length for each batch row, 2: a byte for
+// each key (and perhaps a length).
+template <int D, int MASK>
 __global__ void __launch_bounds__(kCrossThreads, 1)
     cross_fwd_tc_kernel(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossFwdArgs args) {
   using Lay = CrossFwdLayout<D>;
   constexpr int DH = D / 64;
+  constexpr bool MASKED = MASK > 0;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::BAR_OFF + Lay::NBAR * 8);
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lay::NBAR; ++i) {
       // the softmax and epilogue warps arrive one by one
-      const int count = (i >= Lay::PF && i < Lay::OF) || (i >= Lay::OE && i < Lay::DRAIN) ? 4 : 1;
+      const int count = (i >= Lay::PF && i < Lay::OF) || (i >= Lay::OE && i < Lay::WF) ? 4 : 1;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -180,19 +186,24 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     } else if (warp == 14) {
       // ============================================================== masked value rows to zero
       if (MASKED) {
-        uint32_t e[2] = {0, 0};
-        // masked scores are replaced, so key tiles are passed on as they are
-        auto pass = [&](int x, bool value, int b, int row, int limit) -> bool {
+        uint32_t e[2] = {0, 0}, blocks[2] = {0, 0};
+        // a key tile: the masks of its block go to the softmax warps, which replace masked scores, so
+        // the tile is passed on as it is. A block's place is free again: its key tile came into a
+        // ring slot that the softmax of at least kCrossWords - 1 - NKV / 2 blocks before is behind.
+        auto pass = [&](int x, bool value, const uint32_t (&w)[4]) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
-          const bool ok = cross_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to);
-          if (!__all_sync(0xffffffffu, ok)) return false;
+          if (!cross_warp_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to)) return false;
           if (value) {
-            uint32_t w[4];
-            block_words(limit - row, args.mask.keys == nullptr ? nullptr : args.mask.keys + b * args.mask.stride + row,
-                        lane, w);
             zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
-            __syncwarp();
+          } else {
+            const uint32_t at = x * kCrossWords + (x ? blocks[1] : blocks[0]) % kCrossWords;
+            if (MASK == 2 && lane == 0) {
+              st_shared_v4(sbase + Lay::WORD_OFF + at * 16, w[0], w[1], w[2], w[3]);
+              mbar_arrive(&bars[Lay::WF + at]);
+            }
+            x ? ++blocks[1] : ++blocks[0];
           }
+          __syncwarp();
           if (lane == 0) mbar_arrive(&bars[Lay::RDY + s]);
           x ? ++e[1] : ++e[0];
           return true;
@@ -202,11 +213,19 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           const CrossItem it = cross_item(plan, args.heads, i);
           const int len = len_of(it.b);
           const CrossRange r = cross_range(plan, len, it.sp[0]);
+          const unsigned char* keys = MASK < 2 ? nullptr : args.mask.keys + it.b * args.mask.stride;
+          uint32_t last[2][4] = {};  // masks of each job's block k - 1, for its values
           for (int k = 0; ok && k <= r.nk; ++k)
-            for (int x = 0; ok && x < ring.count; ++x) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || x >= ring.count) continue;
               const int row = (r.k0 + x * r.nk + k) * 128;
-              if (k > 0) ok = pass(x, true, it.b, row - 128, len);
-              if (ok && k < r.nk) ok = pass(x, false, it.b, row, len);
+              uint32_t w[4] = {0u, 0u, 0u, 0u};
+              if (k < r.nk) block_words(len - row, keys == nullptr ? nullptr : keys + row, lane, w);
+              if (k > 0) ok = pass(x, true, last[x]);
+              if (ok && k < r.nk) ok = pass(x, false, w);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) last[x][z] = w[z];
             }
         }
       }
@@ -453,6 +472,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     const float c2 = args.scale_log2;
     const uint64_t c2x2 = f2(c2, c2);
     uint32_t sc = 0, jobs = 0;  // blocks and jobs so far
+    uint32_t words = 0;         // blocks of the ring so far, also those of items without a job here
     bool ok = true;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return cross_warp_wait(bar, parity, abort_flag, to);
@@ -460,20 +480,33 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
       const CrossItem it = cross_item(plan, args.heads, i);
       const int qt = x ? it.qt[1] : it.qt[0];
-      if (qt < 0) continue;
       const CrossRange r = cross_range(plan, len_of(it.b), x ? it.sp[1] : it.sp[0]);
+      if (qt < 0) {
+        words += uint32_t(r.nk);
+        continue;
+      }
       // a warp whose rows all lie past the last query has nothing to compute
       const bool idle = qt * 128 + (warp & 3) * 32 >= args.n;
-      const unsigned char* keys =
-          !MASKED || args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + r.k0 * 128;
       float m_run = -INFINITY, l_run = 0.f;
       for (int k = 0; k < r.nk; ++k, ++sc) {
-        const int limit = r.limit - (r.k0 + k) * 128;
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-        if (limit < 128 || (MASKED && keys != nullptr))
-          block_words(limit, keys == nullptr ? nullptr : keys + k * 128, lane, w);
         if (!(ok = wwait(&bars[Lay::SF + x], sc & 1))) break;
         tc_fence_after();
+        // Which keys count: all below the length, or what the mask warp says. The mask warp wrote them before
+        // it passed the key tile on, so they are there by now, and the phase is the block's own: its
+        // place is taken again eight blocks later, which this job's products hold back.
+        uint32_t w[4];
+        if (MASK == 2) {
+          const uint32_t at = (ring.count == 2 ? x * kCrossWords : 0u) + words % kCrossWords;
+          if (!(ok = wwait(&bars[Lay::WF + at], (words / kCrossWords) & 1))) break;
+          const uint4 t = ld_shared_v4(sbase + Lay::WORD_OFF + at * 16);
+          w[0] = t.x;
+          w[1] = t.y;
+          w[2] = t.z;
+          w[3] = t.w;
+          ++words;
+        } else {
+          block_words((MASKED ? len_of(it.b) : args.m) - (r.k0 + k) * 128, nullptr, lane, w);
+        }
         if (idle) {
           tc_fence_before();
           if (lane == 0) {
@@ -481,9 +514,12 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           }
           continue;
         }
-        // a block that does not count whole: its masked scores become -inf where they lie (kept
-        // apart from the code below, which most blocks run alone)
-        if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
+        const bool partial = (w[0] & w[1] & w[2] & w[3]) != ~0u;
+        // Without a mask of each key only the last block is partial: its scores past the keys become
+        // -inf where they lie, in a short loop (the code below is fetched for every block and has to
+        // stay small: selects in registers cost the padded 53,680 pair 3%, and save 6% where every
+        // block has holes)
+        if (MASK < 2 && partial) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const uint32_t word = c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
@@ -502,6 +538,13 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait(v[c]);
+        if (MASK == 2 && partial) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((w[c] >> e) & 1u)) v[c][e] = 0xff800000u;
+        }
         float a[8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

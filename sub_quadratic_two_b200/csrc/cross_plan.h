@@ -79,11 +79,10 @@ SQ_HD CrossItem cross_item(const CrossPlan& p, int heads, int i) {
   return it;
 }
 
-// Key blocks [k0, k0 + nk) of a job and the bound its keys lie below, for `len` keys that may
-// count. nk is the same for every job of a batch row and at least 1: a job short of keys runs
-// blocks whose keys are all masked.
+// Key blocks [k0, k0 + nk) of a job, for `len` keys that may count. nk is the same for every job
+// of a batch row and at least 1: a job short of keys runs blocks past the length.
 struct CrossRange {
-  int k0, nk, limit;
+  int k0, nk;
 };
 SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   const int nb = (len + 127) >> 7;
@@ -91,8 +90,6 @@ SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   r.nk = p.splits > 1 ? (nb + p.splits - 1) / p.splits : nb;
   if (r.nk < 1) r.nk = 1;
   r.k0 = sp * r.nk;
-  const int end = (r.k0 + r.nk) * 128;
-  r.limit = end < len ? end : len;
   return r;
 }
 

@@ -39,9 +39,8 @@ int main() {
         if (it.qt[x] >= p.qtiles || r.nk < 1 || (nk >= 0 && nk != r.nk)) return fail("job", i, x, it.qt[x], r.nk);
         if (x == 1 && p.splits > 1 && r.k0 != sq::cross_range(p, len, it.sp[0]).k0 + r.nk) return fail("k0", i, x, r.k0, r.nk);
         nk = r.nk;
-        if (r.limit > len) return fail("limit", i, x, r.limit, len);
         for (int k = r.k0; k < r.k0 + r.nk; ++k) {
-          if (k >= nb || k * 128 >= r.limit) continue;  // all masked
+          if (k >= nb) continue;  // past the length: all masked
           ++seen[(((long long)it.b * heads + it.h) * p.qtiles + it.qt[x]) * 4096 + k];
         }
       }
