@@ -117,31 +117,70 @@ squad_status allow_smem(K kern, int bytes, const sq::HostDevice& dev, std::atomi
 
 // ---------------------------------------------------------------- fp32
 
-template <int D>
+struct FwdWs {
+  int splits;
+  size_t part_lse, total;  // parts of o first
+};
+
+// Rows per thread of the fp32 kernels (16 times as many to a tile): as many as leave one and a half
+// to two blocks for each SM, and as the tiles of a wide head leave room for.
+int f32_rows(const squad_cross_desc* d) {
+  const long long bh = (long long)d->B * d->heads;
+  if (d->d <= 160 && bh * ((d->n + 63) / 64) >= 2 * sq::kCrossPlanSms) return 4;
+  return bh * ((d->n + 31) / 32) >= 3 * sq::kCrossPlanSms / 2 ? 2 : 1;
+}
+
+FwdWs fwd_workspace(const squad_cross_desc* d) {
+  FwdWs w{};
+  const long long bh = (long long)d->B * d->heads;
+  if (d->dtype == SQUAD_BF16) {
+    w.splits = sq::make_cross_plan(d->B, d->heads, d->kv_heads, d->n, d->m).splits;
+  } else {
+    // parts of the keys where the query tiles leave SMs idle, two tiles of keys at least to a part
+    const int rows = 16 * f32_rows(d), tiles = (d->m + sq::kF32Cols - 1) / sq::kF32Cols;
+    const long long blocks = bh * ((d->n + rows - 1) / rows);
+    const long long s = blocks * 2 <= sq::kCrossPlanSms ? sq::kCrossPlanSms / blocks : 1;
+    w.splits = int(s < tiles / 2 ? s : tiles / 2);
+    if (w.splits < 1) w.splits = 1;
+  }
+  if (w.splits <= 1) return w;
+  const size_t rows = size_t(bh) * d->n * w.splits;
+  w.part_lse = align256(rows * d->d * sizeof(float));
+  w.total = w.part_lse + align256(rows * sizeof(float));
+  return w;
+}
+
+template <int D, int R>
 squad_status f32_cross_fwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  auto kern = sq::cross_f32_fwd_kernel<D>;
-  squad_status s = allow_smem(kern, sq::F32Layout<D>::FWD, dev, done);
+  auto kern = sq::cross_f32_fwd_kernel<D, R>;
+  squad_status s = allow_smem(kern, sq::F32Layout<D, R>::FWD, dev, done);
   if (s != SQUAD_OK) return s;
-  const dim3 grid(unsigned((a.n + sq::kF32Rows - 1) / sq::kF32Rows), unsigned(a.heads), unsigned(a.B));
-  kern<<<grid, sq::kF32Threads, sq::F32Layout<D>::FWD, st>>>(a);
+  const dim3 grid(unsigned((a.n + 16 * R - 1) / (16 * R) * a.splits), unsigned(a.heads), unsigned(a.B));
+  kern<<<grid, sq::kF32Threads, sq::F32Layout<D, R>::FWD, st>>>(a);
   SQ_CUDA(cudaGetLastError());
+  if (a.splits > 1) {
+    const long long rows = (long long)a.B * a.heads * a.n;
+    sq::cross_join_kernel<float><<<unsigned((rows + 3) / 4), 128, 0, st>>>(
+        a.part, a.part_lse, a.splits, rows, a.heads, a.n, D, static_cast<float*>(a.o), a.so, a.lse);
+    SQ_CUDA(cudaGetLastError());
+  }
   return SQUAD_OK;
 }
 
-template <int D>
+template <int D, int R>
 squad_status f32_cross_bwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
   static std::atomic<bool> done_q[kMaxDevices], done_kv[kMaxDevices];
-  auto dq = sq::cross_f32_dq_kernel<D>;
-  auto dkv = sq::cross_f32_dkdv_kernel<D>;
+  auto dq = sq::cross_f32_dq_kernel<D, R>;
+  auto dkv = sq::cross_f32_dkdv_kernel<D, R>;
   squad_status s;
-  if ((s = allow_smem(dq, sq::F32Layout<D>::DQ, dev, done_q)) != SQUAD_OK) return s;
-  if ((s = allow_smem(dkv, sq::F32Layout<D>::DKV, dev, done_kv)) != SQUAD_OK) return s;
-  const dim3 gq(unsigned((a.n + sq::kF32Rows - 1) / sq::kF32Rows), unsigned(a.heads), unsigned(a.B));
-  dq<<<gq, sq::kF32Threads, sq::F32Layout<D>::DQ, st>>>(a);
+  if ((s = allow_smem(dq, sq::F32Layout<D, R>::DQ, dev, done_q)) != SQUAD_OK) return s;
+  if ((s = allow_smem(dkv, sq::F32Layout<D, R>::DKV, dev, done_kv)) != SQUAD_OK) return s;
+  const dim3 gq(unsigned((a.n + 16 * R - 1) / (16 * R)), unsigned(a.heads), unsigned(a.B));
+  dq<<<gq, sq::kF32Threads, sq::F32Layout<D, R>::DQ, st>>>(a);
   SQ_CUDA(cudaGetLastError());
-  const dim3 gk(unsigned((a.m + sq::kF32Rows - 1) / sq::kF32Rows * a.splits), unsigned(a.kv_heads), unsigned(a.B));
-  dkv<<<gk, sq::kF32Threads, sq::F32Layout<D>::DKV, st>>>(a);
+  const dim3 gk(unsigned((a.m + 16 * R - 1) / (16 * R) * a.splits), unsigned(a.kv_heads), unsigned(a.B));
+  dkv<<<gk, sq::kF32Threads, sq::F32Layout<D, R>::DKV, st>>>(a);
   SQ_CUDA(cudaGetLastError());
   if (a.splits > 1) {
     const long long rows = (long long)a.B * a.kv_heads * a.m;
@@ -154,11 +193,19 @@ squad_status f32_cross_bwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cu
   return SQUAD_OK;
 }
 
+template <int D, int R, bool BWD>
+squad_status f32_cross_run(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+  return BWD ? f32_cross_bwd<D, R>(dev, a, st) : f32_cross_fwd<D, R>(dev, a, st);
+}
+
 template <bool BWD>
-squad_status f32_cross(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
-#define SQ_D(N) \
-  case N:       \
-    return BWD ? f32_cross_bwd<N>(dev, a, st) : f32_cross_fwd<N>(dev, a, st)
+squad_status f32_cross(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& a, cudaStream_t st) {
+  const int r = f32_rows(d);
+#define SQ_D(N)                                                   \
+  case N:                                                         \
+    return r == 4   ? f32_cross_run<N, (N <= 160 ? 4 : 2), BWD>(dev, a, st) \
+           : r == 2 ? f32_cross_run<N, 2, BWD>(dev, a, st)        \
+                    : f32_cross_run<N, 1, BWD>(dev, a, st)
   switch (a.d) {
     SQ_D(32);
     SQ_D(64);
@@ -189,21 +236,6 @@ squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void
   return sq::host_encode_bf16(map, dev.device, 4, base, dims, strides, box);
 }
 
-struct FwdWs {
-  size_t part_o, part_lse, total;
-};
-
-FwdWs fwd_workspace(const squad_cross_desc* d) {
-  FwdWs w{};
-  if (d->dtype != SQUAD_BF16) return w;
-  const sq::CrossPlan p = sq::make_cross_plan(d->B, d->heads, d->kv_heads, d->n, d->m);
-  if (p.splits <= 1) return w;
-  const size_t rows = size_t(d->B) * d->heads * d->n * p.splits;
-  w.part_lse = align256(rows * d->d * sizeof(float));
-  w.total = w.part_lse + align256(rows * sizeof(float));
-  return w;
-}
-
 template <int D, int MASK>
 squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& maps, const sq::CrossFwdArgs& a,
                               cudaStream_t st) {
@@ -218,7 +250,7 @@ squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& ma
   return SQUAD_OK;
 }
 
-squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c, void* ws,
+squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c,
                           cudaStream_t st) {
   sq::CrossMaps maps;
   sq::CrossFwdArgs a{};
@@ -237,11 +269,8 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.lse = c.lse;
   a.err = dev.err;
   a.timeout_ns = sq::kWaitTimeoutNs;
-  const FwdWs w = fwd_workspace(d);
-  if (a.plan.splits > 1) {
-    a.part_o = static_cast<float*>(ws);
-    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part_lse);
-  }
+  a.part_o = c.part;
+  a.part_lse = c.part_lse;
   const int mask = c.mask.keys != nullptr ? 2 : c.mask.lens != nullptr ? 1 : 0;
   if (d->d == 128)
     s = mask == 2   ? launch_cross_fwd<128, 2>(dev, maps, a, st)
@@ -254,13 +283,8 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   if (s != SQUAD_OK || a.plan.splits <= 1) return s;
   const long long rows = (long long)d->B * d->heads * d->n;
   const unsigned blocks = unsigned((rows + 3) / 4);
-  auto* o = static_cast<__nv_bfloat16*>(c.o);
-  if (d->d == 128)
-    sq::cross_join_kernel<128><<<blocks, 128, 0, st>>>(a.part_o, a.part_lse, a.plan.splits, rows, d->heads, d->n, o,
-                                                       c.so, c.lse);
-  else
-    sq::cross_join_kernel<64><<<blocks, 128, 0, st>>>(a.part_o, a.part_lse, a.plan.splits, rows, d->heads, d->n, o,
-                                                      c.so, c.lse);
+  sq::cross_join_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(a.part_o, a.part_lse, a.plan.splits, rows, d->heads, d->n,
+                                                              d->d, static_cast<__nv_bfloat16*>(c.o), c.so, c.lse);
   SQ_CUDA(cudaGetLastError());
   return SQUAD_OK;
 }
@@ -278,7 +302,7 @@ BwdWs bwd_workspace(const squad_cross_desc* d) {
   w.part = bwd_rowvec_bytes(d);
   w.total = w.part;
   const bool tc = d->dtype == SQUAD_BF16;
-  const int keys = tc ? 128 : sq::kF32Rows, queries = tc ? 128 : sq::kF32Cols;
+  const int keys = tc ? 128 : 16 * f32_rows(d), queries = tc ? 128 : sq::kF32Cols;
   const long long units = (long long)d->B * d->kv_heads * ((d->m + keys - 1) / keys);
   const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + queries - 1) / queries);
   w.splits = sq::cross_dkv_splits(units, int(tiles));
@@ -398,8 +422,12 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
   sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
   a.o = o;
   a.lse = lse;
+  const FwdWs w = fwd_workspace(desc);
+  a.splits = w.splits;
+  a.part = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part_lse);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, workspace, st) : f32_cross<false>(dev, a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, st) : f32_cross<false>(dev, desc, a, st);
 }
 
 squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
@@ -432,7 +460,7 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   a.splits = w.splits;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : f32_cross<true>(dev, a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : f32_cross<true>(dev, desc, a, st);
 }
 
 // ---------------------------------------------------------------- rotary positions

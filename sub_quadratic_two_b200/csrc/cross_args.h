@@ -33,8 +33,10 @@ struct CrossArgs {
   void *o, *dq, *dk, *dv;
   float* lse;   // written by the forward (or nullptr), read by the backward
   float* Drow;  // [B, heads, n], written by the dq kernel for the dk, dv kernel
-  int splits;   // parts of the queries in the dk, dv kernel
-  float* part;  // their dk and dv where there are several
+  // fp32: parts of the keys in the forward, of the queries in the dk, dv kernel; their results
+  // where there are several
+  int splits;
+  float *part, *part_lse;
 };
 
 template <typename T>

@@ -3,11 +3,13 @@
 // For P_ij = exp(s <q_i,k_j> - lse_i) over the keys j that count, dP_ij = <dO_i, v_j>,
 // D_i = <dO_i, O_i> and dS_ij = P_ij (dP_ij - D_i):
 //   o_i = sum_j P_ij v_j,  dq_i = s sum_j dS_ij k_j,  dk_j = s sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i.
-// Tiles of 32 rows (queries; keys in the dk, dv kernel) against 64 of the other side live in
+// Tiles of 16 R rows (queries; keys in the dk, dv kernel) against 64 of the other side live in
 // shared memory, rows padded by 16 bytes so that the 16-byte loads of eight lanes fall into
-// different banks. 256 threads as 16 x 16: thread (y, x) computes the scores of rows y, y + 16
-// and columns x + 16 j, and accumulates rows y, y + 16 of the results in 4-channel groups
-// x + 16 c. The FMA pipe bounds it: 6 shared-memory loads of 16 bytes per 32 FMAs.
+// different banks. 256 threads as 16 x 16: thread (y, x) computes the scores of rows y + 16 i
+// (i < R) and columns x + 16 j, and accumulates its rows of the results in 4-channel groups
+// x + 16 c. R = 2 where that makes two blocks for each SM, else R = 1: half as many FMAs for a
+// shared-memory load, but twice the blocks (XXX against XXX us at 1,000 x 130, 4 heads, forward
+// and backward; at 4,096 x 1,024, 8 heads, XXX against XXX).
 // Keys that do not count are zero-filled instead of read.
 #pragma once
 #include <cstdint>
@@ -16,45 +18,57 @@
 
 namespace sq {
 
-constexpr int kF32Threads = 256, kF32Rows = 32, kF32Cols = 64, kF32P = kF32Cols + 4;
+constexpr int kF32Threads = 256, kF32Cols = 64, kF32P = kF32Cols + 4;
 
-template <int D>
+template <int D, int R = 1>
 struct F32Layout {
   static constexpr int LD = D + 4;                 // floats between rows of a tile
   static constexpr int NC = (D / 4 + 15) / 16;     // 4-channel groups of a thread
-  static constexpr int ROWS = kF32Rows * LD, COLS = kF32Cols * LD, P = kF32Rows * kF32P;
-  static constexpr int FWD = (ROWS + COLS + P + kF32Cols) * 4;
+  static constexpr int NR = 16 * R;                // rows of a tile
+  static constexpr int ROWS = NR * LD, COLS = kF32Cols * LD, P = NR * kF32P;
+  static constexpr int FWD = (ROWS + 2 * COLS + P + kF32Cols) * 4;
   static constexpr int DQ = (2 * ROWS + 2 * COLS + P + kF32Cols) * 4;
   static constexpr int DKV = (2 * ROWS + 2 * COLS + 2 * P + 2 * kF32Cols) * 4;
-  static_assert(DKV <= 232448, "shared memory of one CTA");
 };
 
-// n rows of D floats (row stride in elements) into a padded tile; rows from `valid` on, and rows
-// whose keep entry is 0 (keep may be null), are zero.
+// n rows of D floats (row stride in elements) into a padded tile, by asynchronous copies (every
+// load of a tile is in flight at once; a thread that loads and stores by turns waits for each).
+// Rows from `valid` on, and rows whose keep entry is 0 (keep may be null), are zero.
 template <int D>
 __device__ __forceinline__ void f32_load(float* tile, const float* src, long long stride, int n, int valid,
                                          const float* keep) {
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(tile));
   for (int i = threadIdx.x; i < n * (D / 4); i += kF32Threads) {
     const int r = i / (D / 4), c = i - r * (D / 4);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < valid && (keep == nullptr || keep[r] != 0.f)) v = *reinterpret_cast<const float4*>(src + r * stride + 4 * c);
-    *reinterpret_cast<float4*>(tile + r * F32Layout<D>::LD + 4 * c) = v;
+    const bool live = r < valid && (keep == nullptr || keep[r] != 0.f);
+    // a copy of 0 bytes reads nothing and fills the 16 with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (r * F32Layout<D>::LD + 4 * c) * 4),
+                 "l"(live ? src + r * stride + 4 * c : src), "r"(live ? 16 : 0)
+                 : "memory");
   }
+}
+__device__ __forceinline__ void f32_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for every copy of this thread: none is in flight when a block ends.
+__device__ __forceinline__ void f32_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Waits until at most N of this thread's last groups are in flight.
+template <int N>
+__device__ __forceinline__ void f32_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // s[a][j] += <rows y + 16 a, cols x + 16 j>
-template <int D>
-__device__ __forceinline__ void f32_dots(const float* rows, const float* cols, int y, int x, float (&s)[2][4]) {
+template <int D, int R>
+__device__ __forceinline__ void f32_dots(const float* rows, const float* cols, int y, int x, float (&s)[R][4]) {
   constexpr int LD = F32Layout<D>::LD;
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
-    float4 a[2], b[4];
+    float4 a[R], b[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4*>(rows + (y + 16 * i) * LD + c);
+    for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(rows + (y + 16 * i) * LD + c);
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(cols + (x + 16 * j) * LD + c);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
@@ -62,15 +76,15 @@ __device__ __forceinline__ void f32_dots(const float* rows, const float* cols, i
 }
 
 // acc[a][g] += sum_j p[y + 16 a][j] cols[j][channels 4 (x + 16 g) ..]
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ void f32_accumulate(const float* p, const float* cols, int y, int x,
-                                               float4 (&acc)[2][F32Layout<D>::NC]) {
+                                               float4 (&acc)[R][F32Layout<D>::NC]) {
   constexpr int LD = F32Layout<D>::LD, NC = F32Layout<D>::NC;
 #pragma unroll 2
   for (int j = 0; j < kF32Cols; j += 4) {
-    float w[2][4];
+    float w[R][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < R; ++i) {
       const float4 t = *reinterpret_cast<const float4*>(p + (y + 16 * i) * kF32P + j);
       w[i][0] = t.x;
       w[i][1] = t.y;
@@ -84,7 +98,7 @@ __device__ __forceinline__ void f32_accumulate(const float* p, const float* cols
         if (D % 64 != 0 && x + 16 * g >= D / 4) continue;
         const float4 v = *reinterpret_cast<const float4*>(cols + (j + e) * LD + 4 * (x + 16 * g));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
           acc[i][g].x = fmaf(w[i][e], v.x, acc[i][g].x);
           acc[i][g].y = fmaf(w[i][e], v.y, acc[i][g].y);
           acc[i][g].z = fmaf(w[i][e], v.z, acc[i][g].z);
@@ -107,26 +121,41 @@ __device__ __forceinline__ void f32_keep(float* keep, int n, const CrossMask& mk
     keep[threadIdx.x] = j0 + int(threadIdx.x) < len && cross_keeps(mk, b, j0 + threadIdx.x) ? 1.f : 0.f;
 }
 
-template <int D>
+// With a.splits > 1 the keys of a query tile are cut into parts (blockIdx.x = query tile * splits +
+// part), whose results and log-sums (base 2) go to a.part and a.part_lse, [part][B, heads, n].
+template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cross_f32_fwd_kernel(const __grid_constant__ CrossArgs a) {
-  using Lay = F32Layout<D>;
+  using Lay = F32Layout<D, R>;
   extern __shared__ __align__(16) float f32_smem[];
-  float *qs = f32_smem, *kv = qs + Lay::ROWS, *ps = kv + Lay::COLS, *keep = ps + Lay::P;
-  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = blockIdx.x * kF32Rows;
+  float *qs = f32_smem, *ks = qs + Lay::ROWS, *vs = ks + Lay::COLS, *ps = vs + Lay::COLS, *keep = ps + Lay::P;
+  const int qt = blockIdx.x / a.splits, sp = blockIdx.x - qt * a.splits;
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = qt * Lay::NR;
   const int y = threadIdx.x >> 4, x = threadIdx.x & 15, len = cross_len(a.mask, b, a.m);
-  f32_load<D>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, kF32Rows, a.n - i0, nullptr);
-  float4 acc[2][Lay::NC] = {};
-  float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  for (int j0 = 0; j0 < len; j0 += kF32Cols) {
+  // this part's keys: whole tiles of them
+  const int tiles = (len + kF32Cols - 1) / kF32Cols, per = (tiles + a.splits - 1) / a.splits * kF32Cols;
+  const int k0 = sp * per, k1 = k0 + per < len ? k0 + per : len;
+  f32_load<D>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, Lay::NR, a.n - i0, nullptr);
+  float4 acc[R][Lay::NC] = {};
+  float mx[R], l[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    mx[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  for (int j0 = k0; j0 < k1; j0 += kF32Cols) {
     __syncthreads();  // the last tile's values are done with
     f32_keep(keep, kF32Cols, a.mask, b, j0, len);
     __syncthreads();
-    f32_load<D>(kv, cross_row<float>(a.k, a.sk, b, hk, j0), a.sk.n, kF32Cols, a.m - j0, keep);
+    f32_load<D>(ks, cross_row<float>(a.k, a.sk, b, hk, j0), a.sk.n, kF32Cols, a.m - j0, keep);
+    f32_commit();
+    f32_load<D>(vs, cross_row<float>(a.v, a.sv, b, hk, j0), a.sv.n, kF32Cols, a.m - j0, keep);
+    f32_commit();
+    f32_wait<1>();  // the keys (and the queries) are there, the values may still come
     __syncthreads();
-    float s[2][4] = {};
-    f32_dots<D>(qs, kv, y, x, s);
+    float s[R][4] = {};
+    f32_dots<D, R>(qs, ks, y, x, s);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < R; ++i) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -154,43 +183,51 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_fwd_kernel(const __grid
         acc[i][g].w *= corr;
       }
     }
-    __syncthreads();  // the scores are made: the values take the keys' place
-    f32_load<D>(kv, cross_row<float>(a.v, a.sv, b, hk, j0), a.sv.n, kF32Cols, a.m - j0, keep);
+    f32_wait<0>();
     __syncthreads();
-    f32_accumulate<D>(ps, kv, y, x, acc);
+    f32_accumulate<D, R>(ps, vs, y, x, acc);
   }
+  f32_wait_all();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int r = i0 + y + 16 * i;
     if (r >= a.n) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];
-    float* out = cross_row<float>(a.o, a.so, b, h, r);
+    const long long row = ((long long)b * a.heads + h) * a.n + r, part_row = (long long)sp * a.B * a.heads * a.n + row;
+    float* out = a.splits > 1 ? a.part + part_row * D : cross_row<float>(a.o, a.so, b, h, r);
 #pragma unroll
     for (int g = 0; g < Lay::NC; ++g) {
       if (D % 64 != 0 && x + 16 * g >= D / 4) continue;
       *reinterpret_cast<float4*>(out + 4 * (x + 16 * g)) =
           make_float4(acc[i][g].x * inv, acc[i][g].y * inv, acc[i][g].z * inv, acc[i][g].w * inv);
     }
-    if (a.lse != nullptr && x == 0)
-      a.lse[((long long)b * a.heads + h) * a.n + r] = l[i] == 0.f ? -INFINITY : mx[i] + logf(l[i]);
+    const float lse = l[i] == 0.f ? -INFINITY : mx[i] + logf(l[i]);
+    if (x == 0) {
+      if (a.splits > 1)
+        a.part_lse[part_row] = lse * 1.4426950408889634f;
+      else if (a.lse != nullptr)
+        a.lse[row] = lse;
+    }
   }
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_constant__ CrossArgs a) {
-  using Lay = F32Layout<D>;
+  using Lay = F32Layout<D, R>;
   extern __shared__ __align__(16) float f32_smem[];
   float *qs = f32_smem, *dos = qs + Lay::ROWS, *ks = dos + Lay::ROWS, *vs = ks + Lay::COLS, *ps = vs + Lay::COLS,
         *keep = ps + Lay::P;
-  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = blockIdx.x * kF32Rows;
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = blockIdx.x * Lay::NR;
   const int y = threadIdx.x >> 4, x = threadIdx.x & 15, len = cross_len(a.mask, b, a.m);
-  f32_load<D>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, kF32Rows, a.n - i0, nullptr);
-  f32_load<D>(dos, cross_row<float>(a.dout, a.sdo, b, h, i0), a.sdo.n, kF32Rows, a.n - i0, nullptr);
+  f32_load<D>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, Lay::NR, a.n - i0, nullptr);
+  f32_load<D>(dos, cross_row<float>(a.dout, a.sdo, b, h, i0), a.sdo.n, Lay::NR, a.n - i0, nullptr);
+  f32_commit();
+  f32_wait<0>();
   __syncthreads();
-  float dd[2], lse[2];
+  float dd[R], lse[R];
   const long long base = ((long long)b * a.heads + h) * a.n;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int r = i0 + y + 16 * i;
     float t = 0.f;
     lse[i] = INFINITY;  // rows past the last, and rows without keys: P = 0
@@ -203,29 +240,31 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
     dd[i] = f32_row_sum(t);
     if (r < a.n && x == 0) a.Drow[base + r] = dd[i];
   }
-  float4 acc[2][Lay::NC] = {};
+  float4 acc[R][Lay::NC] = {};
   for (int j0 = 0; j0 < len; j0 += kF32Cols) {
     __syncthreads();
     f32_keep(keep, kF32Cols, a.mask, b, j0, len);
     __syncthreads();
     f32_load<D>(ks, cross_row<float>(a.k, a.sk, b, hk, j0), a.sk.n, kF32Cols, a.m - j0, keep);
     f32_load<D>(vs, cross_row<float>(a.v, a.sv, b, hk, j0), a.sv.n, kF32Cols, a.m - j0, keep);
+    f32_commit();
+    f32_wait<0>();
     __syncthreads();
-    float s[2][4] = {}, dp[2][4] = {};
-    f32_dots<D>(qs, ks, y, x, s);
-    f32_dots<D>(dos, vs, y, x, dp);
+    float s[R][4] = {}, dp[R][4] = {};
+    f32_dots<D, R>(qs, ks, y, x, s);
+    f32_dots<D, R>(dos, vs, y, x, dp);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = keep[x + 16 * j] != 0.f ? expf(s[i][j] * a.scale - lse[i]) : 0.f;
         ps[(y + 16 * i) * kF32P + x + 16 * j] = p * (dp[i][j] - dd[i]);
       }
     __syncthreads();
-    f32_accumulate<D>(ps, ks, y, x, acc);
+    f32_accumulate<D, R>(ps, ks, y, x, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int r = i0 + y + 16 * i;
     if (r >= a.n) continue;
     float* out = cross_row<float>(a.dq, a.sdq, b, h, r);
@@ -238,23 +277,23 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
   }
 }
 
-// A block: 32 keys and one part of the queries of their head group (blockIdx.x = key tile *
+// A block: 16 R keys and one part of the queries of their head group (blockIdx.x = key tile *
 // splits + part); with splits > 1 the parts go to a.part, [dk, dv][split][B, kv_heads, m][D].
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cross_f32_dkdv_kernel(const __grid_constant__ CrossArgs a) {
-  using Lay = F32Layout<D>;
+  using Lay = F32Layout<D, R>;
   extern __shared__ __align__(16) float f32_smem[];
   float *ks = f32_smem, *vs = ks + Lay::ROWS, *qs = vs + Lay::ROWS, *dos = qs + Lay::COLS, *ps = dos + Lay::COLS,
         *dss = ps + Lay::P, *lse = dss + Lay::P, *dd = lse + kF32Cols;
-  __shared__ float keep[kF32Rows];
+  __shared__ float keep[Lay::NR];
   const int b = blockIdx.z, hk = blockIdx.y, kt = blockIdx.x / a.splits, sp = blockIdx.x - kt * a.splits;
-  const int j0 = kt * kF32Rows, y = threadIdx.x >> 4, x = threadIdx.x & 15, len = cross_len(a.mask, b, a.m);
-  f32_keep(keep, kF32Rows, a.mask, b, j0, len);
+  const int j0 = kt * Lay::NR, y = threadIdx.x >> 4, x = threadIdx.x & 15, len = cross_len(a.mask, b, a.m);
+  f32_keep(keep, Lay::NR, a.mask, b, j0, len);
   __syncthreads();
-  float4 dk[2][Lay::NC] = {}, dv[2][Lay::NC] = {};
+  float4 dk[R][Lay::NC] = {}, dv[R][Lay::NC] = {};
   if (j0 < len) {
-    f32_load<D>(ks, cross_row<float>(a.k, a.sk, b, hk, j0), a.sk.n, kF32Rows, a.m - j0, keep);
-    f32_load<D>(vs, cross_row<float>(a.v, a.sv, b, hk, j0), a.sv.n, kF32Rows, a.m - j0, keep);
+    f32_load<D>(ks, cross_row<float>(a.k, a.sk, b, hk, j0), a.sk.n, Lay::NR, a.m - j0, keep);
+    f32_load<D>(vs, cross_row<float>(a.v, a.sv, b, hk, j0), a.sv.n, Lay::NR, a.m - j0, keep);
     const int qtiles = (a.n + kF32Cols - 1) / kF32Cols, tiles = a.group * qtiles;
     const int per = (tiles + a.splits - 1) / a.splits;
     const int t1 = (sp + 1) * per < tiles ? (sp + 1) * per : tiles;
@@ -270,12 +309,14 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dkdv_kernel(const __gri
       }
       f32_load<D>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, kF32Cols, a.n - i0, nullptr);
       f32_load<D>(dos, cross_row<float>(a.dout, a.sdo, b, h, i0), a.sdo.n, kF32Cols, a.n - i0, nullptr);
+      f32_commit();
+      f32_wait<0>();  // the keys' tiles too, at the first turn
       __syncthreads();
-      float s[2][4] = {}, dp[2][4] = {};
-      f32_dots<D>(ks, qs, y, x, s);
-      f32_dots<D>(vs, dos, y, x, dp);
+      float s[R][4] = {}, dp[R][4] = {};
+      f32_dots<D, R>(ks, qs, y, x, s);
+      f32_dots<D, R>(vs, dos, y, x, dp);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = x + 16 * j;
@@ -284,13 +325,14 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dkdv_kernel(const __gri
           dss[(y + 16 * i) * kF32P + c] = p * (dp[i][j] - dd[c]);
         }
       __syncthreads();
-      f32_accumulate<D>(ps, dos, y, x, dv);
-      f32_accumulate<D>(dss, qs, y, x, dk);
+      f32_accumulate<D, R>(ps, dos, y, x, dv);
+      f32_accumulate<D, R>(dss, qs, y, x, dk);
     }
   }
+  f32_wait_all();
   const long long rows = (long long)a.B * a.kv_heads * a.m;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int j = j0 + y + 16 * i;
     if (j >= a.m) continue;
     const long long row = ((long long)b * a.kv_heads + hk) * a.m + j;

@@ -624,12 +624,12 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
 }
 
 // Joins the key splits of a row: o = sum_s 2^(l_s - max) o_s / sum_s 2^(l_s - max), with
-// l_s = log2 of the split's sum. One warp per row, lanes over the channels.
-template <int D>
+// l_s = log2 of the split's sum. One warp per row, its lanes over the channels.
+template <typename T>
 __global__ void __launch_bounds__(128) cross_join_kernel(const float* __restrict__ part_o,
                                                          const float* __restrict__ part_lse, int splits,
-                                                         long long rows, int heads, int n, __nv_bfloat16* o,
-                                                         CrossStride so, float* lse) {
+                                                         long long rows, int heads, int n, int D, T* o, CrossStride so,
+                                                         float* lse) {
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -637,26 +637,27 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const float* __restrict
   for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, part_lse[s * rows + row]);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-  constexpr int C = D / 32;
-  float acc[C], total = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  if (mx != -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
-      const float wt = exp2f(part_lse[s * rows + row] - mx);
-      total += wt;
-      const float* p = part_o + (s * rows + row) * D + lane * C;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] = fmaf(wt, p[c], acc[c]);
-    }
-  }
+  float total = 0.f;
+  if (mx != -INFINITY)
+    for (int s = 0; s < splits; ++s) total += exp2f(part_lse[s * rows + row] - mx);
   const float inv = total > 0.f ? 1.f / total : total;
   const long long bh = row / n;
   const int i = int(row - bh * n), b = int(bh / heads), h = int(bh - (long long)b * heads);
-  __nv_bfloat16* out = o + b * so.b + h * so.h + i * so.n + lane * C;
-#pragma unroll
-  for (int c = 0; c < C; c += 2)
-    *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  T* out = o + b * so.b + h * so.h + i * so.n;
+  for (int c = 2 * lane; c < D; c += 64) {
+    float2 acc = make_float2(0.f, 0.f);
+    if (mx != -INFINITY)
+      for (int s = 0; s < splits; ++s) {
+        const float wt = exp2f(part_lse[s * rows + row] - mx);
+        const float2 p = *reinterpret_cast<const float2*>(part_o + (s * rows + row) * D + c);
+        acc.x = fmaf(wt, p.x, acc.x);
+        acc.y = fmaf(wt, p.y, acc.y);
+      }
+    if (sizeof(T) == 2)
+      *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(acc.x * inv, acc.y * inv);
+    else
+      *reinterpret_cast<float2*>(out + c) = make_float2(acc.x * inv, acc.y * inv);
+  }
   if (lse != nullptr && lane == 0) lse[row] = total > 0.f ? (mx + log2f(total)) * 0.69314718055994530942f : mx;
 }
 
