@@ -116,13 +116,13 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
 
     desc, nb = _call((q, k, v, out), kv_lens, key_mask, scale, build)
     o = empty_like_layout(q) if out is None else out
-    lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32) if save else None
+    lse = q.new_empty(q.shape[:3], dtype=torch.float32) if save else None
     if desc is None:  # no query, or no key for any of them
         o.zero_()
         if save:
             lse.fill_(float("-inf"))
         return o, lse
-    ws = torch.empty(nb, device=q.device, dtype=torch.uint8) if nb else None
+    ws = q.new_empty(nb, dtype=torch.uint8) if nb else None
     with on_device(q.device):
         _check(load_library().squad_cross_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                               _at(kv_lens), _at(key_mask), o.data_ptr(), _at(lse), _at(ws), nb,
@@ -154,7 +154,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
     dq, dk, dv = empty_like_layout(q), empty_like_layout(k), empty_like_layout(v)
     if desc is None:
         return dq.zero_(), dk.zero_(), dv.zero_()
-    ws = torch.empty(nb, device=q.device, dtype=torch.uint8)
+    ws = q.new_empty(nb, dtype=torch.uint8)
     with on_device(q.device):
         _check(load_library().squad_cross_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                               _at(kv_lens), _at(key_mask), o.data_ptr(), lse.data_ptr(),

@@ -7,9 +7,10 @@
 // shared memory, rows padded by 16 bytes so that the 16-byte loads of eight lanes fall into
 // different banks. 256 threads as 16 x 16: thread (y, x) computes the scores of rows y + 16 i
 // (i < R) and columns x + 16 j, and accumulates its rows of the results in 4-channel groups
-// x + 16 c. R = 2 where that makes two blocks for each SM, else R = 1: half as many FMAs for a
-// shared-memory load, but twice the blocks (XXX against XXX us at 1,000 x 130, 4 heads, forward
-// and backward; at 4,096 x 1,024, 8 heads, XXX against XXX).
+// x + 16 c. Shared-memory loads bound it (a 16-byte load of a warp takes four passes, shared
+// addresses or not): (R + 4) of them for 16 R FMAs. A larger R saves loads, a smaller one gives
+// more blocks; forward + backward at 4,096 x 1,024, 8 heads of 128: 5.47 ms with R = 1, 3.28 with 2,
+// 2.59 with 4 (28 TFLOP/s forward); at 1,000 x 130, 4 heads of 96: 124 us with 1, 134 with 2.
 // Keys that do not count are zero-filled instead of read.
 #pragma once
 #include <cstdint>

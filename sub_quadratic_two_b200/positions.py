@@ -49,9 +49,7 @@ def empty_like_layout(t: torch.Tensor) -> torch.Tensor:
     if t.is_contiguous():
         return torch.empty_like(t)
     B, h, n, d = t.shape
-    if token_major(t):
-        return torch.empty((B, n, h, d), device=t.device, dtype=t.dtype).transpose(1, 2)
-    return torch.empty((B, h, n, d), device=t.device, dtype=t.dtype)
+    return t.new_empty_strided((B, h, n, d), (n * h * d, d, h * d, 1) if token_major(t) else (h * n * d, n * d, d, 1))
 
 
 def check_strided(*named):
@@ -176,7 +174,7 @@ def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
         with torch.cuda.stream(stream):
             return squad_rotary(xs, rot, inverse, out)
     if out is None:
-        ys = [torch.empty(x.shape, device=x.device, dtype=x.dtype) for x in xs]
+        ys = [x.new_empty(x.shape) for x in xs]
     else:
         ys = list(out)
     if not xs:
@@ -217,8 +215,8 @@ class _Rotary(torch.autograd.Function):
             ys = []
             for i, g in zip(take, gs):
                 B, h, n, d = g.shape
-                y = torch.empty((B, n, h, d) if ctx.token_major[i] else (B, h, n, d), device=g.device, dtype=g.dtype)
-                ys.append(y.transpose(1, 2) if ctx.token_major[i] else y)
+                ys.append(g.new_empty_strided((B, h, n, d), (n * h * d, d, h * d, 1)) if ctx.token_major[i]
+                          else g.new_empty((B, h, n, d)))
             for i, y in zip(take, squad_rotary(gs, ctx.rot, inverse=True, out=ys)):
                 out[i] = y
         return (None, *out)
