@@ -140,7 +140,8 @@ FwdWs fwd_workspace(const squad_cross_desc* d) {
     const int rows = 16 * f32_rows(d), tiles = (d->m + sq::kF32Cols - 1) / sq::kF32Cols;
     const long long blocks = bh * ((d->n + rows - 1) / rows);
     const long long s = blocks * 2 <= sq::kCrossPlanSms ? sq::kCrossPlanSms / blocks : 1;
-    w.splits = int(s < tiles / 2 ? s : tiles / 2);
+    const long long most = tiles / 2 < 64 ? tiles / 2 : 64;
+    w.splits = int(s < most ? s : most);
     if (w.splits < 1) w.splits = 1;
   }
   if (w.splits <= 1) return w;

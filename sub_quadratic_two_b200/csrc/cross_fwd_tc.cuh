@@ -633,32 +633,43 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const float* __restrict
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  float mx = -INFINITY;
-  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, part_lse[s * rows + row]);
+  // lane s holds the weights of splits s and s + 32 (there are at most 64)
+  const float l0 = lane < splits ? part_lse[lane * rows + row] : -INFINITY;
+  const float l1 = lane + 32 < splits ? part_lse[(lane + 32) * rows + row] : -INFINITY;
+  float mx = fmaxf(l0, l1);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-  float total = 0.f;
-  if (mx != -INFINITY)
-    for (int s = 0; s < splits; ++s) total += exp2f(part_lse[s * rows + row] - mx);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  const float w0 = exp2f(l0 - ref), w1 = exp2f(l1 - ref);
+  float total = w0 + w1;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
   const float inv = total > 0.f ? 1.f / total : total;
   const long long bh = row / n;
   const int i = int(row - bh * n), b = int(bh / heads), h = int(bh - (long long)b * heads);
   T* out = o + b * so.b + h * so.h + i * so.n;
-  for (int c = 2 * lane; c < D; c += 64) {
-    float2 acc = make_float2(0.f, 0.f);
-    if (mx != -INFINITY)
-      for (int s = 0; s < splits; ++s) {
-        const float wt = exp2f(part_lse[s * rows + row] - mx);
-        const float2 p = *reinterpret_cast<const float2*>(part_o + (s * rows + row) * D + c);
+  for (int c0 = 0; c0 < D; c0 += 128) {
+    const int c = c0 + 4 * lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float wt = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+      if (c < D) {
+        const float4 p = *reinterpret_cast<const float4*>(part_o + (s * rows + row) * D + c);
         acc.x = fmaf(wt, p.x, acc.x);
         acc.y = fmaf(wt, p.y, acc.y);
+        acc.z = fmaf(wt, p.z, acc.z);
+        acc.w = fmaf(wt, p.w, acc.w);
       }
+    }
+    if (c >= D) continue;
     if (sizeof(T) == 2)
-      *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(acc.x * inv, acc.y * inv);
+      *reinterpret_cast<uint2*>(out + c) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     else
-      *reinterpret_cast<float2*>(out + c) = make_float2(acc.x * inv, acc.y * inv);
+      *reinterpret_cast<float4*>(out + c) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   }
-  if (lse != nullptr && lane == 0) lse[row] = total > 0.f ? (mx + log2f(total)) * 0.69314718055994530942f : mx;
+  if (lse != nullptr && lane == 0) lse[row] = total == 0.f ? mx : (mx + log2f(total)) * 0.69314718055994530942f;
 }
 
 }  // namespace sq

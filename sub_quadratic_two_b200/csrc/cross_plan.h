@@ -3,9 +3,15 @@
 // A job is one 128-query tile over a range of 128-key blocks; an item is two jobs of one
 // (batch, head), run side by side on one SM. Where the query tiles fill the SMs, the jobs of
 // an item are two neighbouring tiles over all keys, which share the key and value tiles in
-// shared memory. Where they do not, an item takes one tile alone (a second SM is better than
-// a shared tile), and where even that leaves SMs idle the keys of a tile are split over
-// `splits` jobs, whose partial results a second kernel joins.
+// shared memory. Where there are no more tiles than SMs, an item takes one tile alone: a second
+// SM is better than a shared tile (24 heads, d = 128, single / pairs: 144 tiles of 768 queries over
+// 1,024 keys 20.6 / 22.7 us; 216 tiles of 1,100 over 512 keys 20.6 / 14.5). Where the keys are
+// long as well, they are
+// split over `splits` jobs, whose partial results a second kernel joins. The join and the fp32
+// parts cost 4 to 10 us, more with more rows, and a key block saves 1.5 us at most, so the
+// number of key blocks that makes a split worth it grows with the tiles (24 heads, d = 128,
+// whole / split: 1 query x 512 keys 12.4 / 13.4 us, x 1,024 18.5 / 14.5, x 27,280 350 / 61;
+// 384 x 1,024 18.6 / 20.6, x 4,096 57.5 / 32.9; 768 x 2,048 32.9 / 35.0, x 4,096 59.5 / 49.3).
 #pragma once
 #include <cstdint>
 #include "geometry.h"
@@ -37,9 +43,9 @@ inline CrossPlan make_cross_plan(int B, int heads, int kv_heads, int n, int m) {
   p.qtiles = (n + 127) / 128;
   p.kblocks = (m + 127) / 128;
   const long long all = (long long)B * heads * p.qtiles;
-  p.tiles = all >= 2 * kCrossPlanSms ? 2 : 1;
+  p.tiles = all > kCrossPlanSms ? 2 : 1;
   p.splits = 1;
-  if (all * 2 <= kCrossPlanSms && p.kblocks >= 4) {
+  if (all <= kCrossPlanSms && p.kblocks >= 8 && (long long)p.kblocks * kCrossPlanSms >= 32 * all) {
     long long s = 2 * kCrossPlanSms / all;             // two jobs per SM
     const long long most = p.kblocks / 2;              // at least two blocks per job
     s = s < most ? s : most;
