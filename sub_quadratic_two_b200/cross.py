@@ -6,6 +6,7 @@ from functools import lru_cache
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _check_aux, _dtype_code, load_library
 from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout, on_device, raw_stream
@@ -95,11 +96,12 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
                     stream: Optional[torch.cuda.Stream] = None):
     """Cross attention forward through the C ABI. Returns (o, lse); lse is None when save=False.
 
-    o lies in memory as q does (token-major or head-major), or in ``out``.
+    o lies in memory as q does (token-major or head-major), or in ``out``, which must not overlap an input.
     """
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
+    scale = float(scale or 0.0)  # a call is kept by its value
 
     def build():
         step = _check_cross(q, k, v, kv_lens, key_mask)
@@ -111,7 +113,7 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
         code = _dtype_code(q)
         if q.numel() == 0 or k.numel() == 0:
             return None, 0
-        desc = _desc(q.shape, k.shape, code, float(scale or 0.0), step, (q.stride(), k.stride(), v.stride(), o.stride()))
+        desc = _desc(q.shape, k.shape, code, scale, step, (q.stride(), k.stride(), v.stride(), o.stride()))
         return desc, _workspace(tuple(q.shape), tuple(k.shape), code, 0)
 
     desc, nb = _call((q, k, v, out), kv_lens, key_mask, scale, build)
@@ -136,6 +138,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
+    scale = float(scale or 0.0)
 
     def build():
         step = _check_cross(q, k, v, kv_lens, key_mask)
@@ -147,7 +150,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
         if q.numel() == 0 or k.numel() == 0:
             return None, 0
         strides = [t.stride() for t in (q, k, v, o, dout)] + [empty_like_layout(t).stride() for t in (q, k, v)]
-        return (_desc(q.shape, k.shape, code, float(scale or 0.0), step, strides),
+        return (_desc(q.shape, k.shape, code, scale, step, strides),
                 _workspace(tuple(q.shape), tuple(k.shape), code, 1))
 
     desc, nb = _call((q, k, v, o, lse, dout), kv_lens, key_mask, scale, build)
@@ -174,6 +177,7 @@ class _CrossAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, kv_lens, key_mask = ctx.saved_tensors
         if not dense_enough(dout, dout.shape[3]):
@@ -188,7 +192,10 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Op
     float32 or bfloat16 CUDA tensors, n and m free of each other, heads a multiple of kv_heads. Rows may be
     strided (token-major [B, n, heads, d] memory seen through transpose(1, 2)); the output lies as q does.
     kv_lens: [B] int32, the states of each batch row that count; key_mask: [B, m] (or [1, m]) bool, True
-    where a state counts. A query with no state left gets zeros and gives no gradient.
+    where a state counts. A query with no state left gets zeros and gives no gradient. Gradients are not
+    differentiable again. A step captured into a CUDA graph takes its gradients for leaves of its own
+    (``t.detach().requires_grad_()`` shares t's memory): a leaf that an eager graph still holds ties torch's
+    autograd to the stream of that graph, outside the capture, and the capture fails.
     """
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _CrossAttention.apply(q, k, v, scale, kv_lens, key_mask)

@@ -12,6 +12,7 @@ from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _dtype_code, load_library
 
@@ -189,7 +190,10 @@ def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
         if len(_calls) >= 1024:
             _calls.clear()
         _calls[key] = call
-    if ref.shape[0] == 0 or any([x.shape[1] == 0 for x in xs]):
+    if any([x.numel() == 0 for x in xs]):
+        full = [i for i, x in enumerate(xs) if x.numel()]
+        if full:  # one of the two has no heads
+            squad_rotary([xs[i] for i in full], rot, inverse, [ys[i] for i in full])
         return ys
     desc, c, heads, sx, sy, pointers = call
     with on_device(ref.device):
@@ -203,11 +207,14 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rot, *xs):
         ctx.rot = rot
+        ctx.save_for_backward(rot.table)
         ctx.token_major = [token_major(x) for x in xs]
         return tuple(squad_rotary(xs, rot))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
+        ctx.saved_tensors  # raises where the table was changed in the meantime
         out = [None] * len(grads)
         take = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[1 + i]]
         if take:
