@@ -62,6 +62,14 @@ def _check_cross(q, k, v, kv_lens, key_mask) -> int:
     return step
 
 
+def _scale(scale) -> float:
+    """The scale as a number (a call is kept by its value); 0 stands for 1/sqrt(d)."""
+    scale = float(scale or 0.0)
+    if scale < 0:
+        raise ValueError("scale must be positive")
+    return scale
+
+
 def _kind(t: Optional[torch.Tensor]):
     """What the checks look at in a tensor."""
     return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
@@ -101,7 +109,7 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
-    scale = float(scale or 0.0)  # a call is kept by its value
+    scale = _scale(scale)
 
     def build():
         step = _check_cross(q, k, v, kv_lens, key_mask)
@@ -138,7 +146,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
-    scale = float(scale or 0.0)
+    scale = _scale(scale)
 
     def build():
         step = _check_cross(q, k, v, kv_lens, key_mask)

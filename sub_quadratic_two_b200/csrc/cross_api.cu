@@ -363,7 +363,7 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   if ((s = encode_rows(&maps.k, dev, c.k, d->k, B, hk, d->m, D, &a.k_b, &a.k_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.v, dev, c.v, d->v, B, hk, d->m, D, &a.v_b, &a.v_h)) != SQUAD_OK) return s;
   if ((s = encode_rows(&maps.dout, dev, c.dout, d->dout, B, h, d->n, D, &a.do_b, &a.do_h)) != SQUAD_OK) return s;
-a.mask = c.mask;
+  a.mask = c.mask;
   a.scale = c.scale;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.o = static_cast<const __nv_bfloat16*>(c.o_in);

@@ -172,6 +172,8 @@ def test_scale_is_taken_by_value(cuda_ok):
         assert torch.equal(o, r)
         for a, b in zip(sq.squad_cross_bwd(q, k, v, o, lse, do, scale), sq.squad_cross_bwd(q, k, v, o, lse, do, float(scale))):
             assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        sq.cross_attention(q, k, v, scale=-0.1)
 
 
 def test_gradients_are_not_differentiable_again(cuda_ok):
