@@ -240,7 +240,7 @@ squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void
 template <int D, int MASK>
 squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& maps, const sq::CrossFwdArgs& a,
                               cudaStream_t st) {
-  using Lay = sq::CrossFwdLayout<D>;
+  using Lay = sq::CrossFwdLayout<D, MASK>;
   auto kern = sq::cross_fwd_tc_kernel<D, MASK>;
   static std::atomic<bool> done[kMaxDevices];
   squad_status s = allow_smem(kern, Lay::BYTES, dev, done);

@@ -38,6 +38,7 @@ namespace sq {
 
 constexpr int kCrossThreads = 512;
 constexpr int kCrossWords = 8;  // blocks whose masks are kept
+constexpr int kCrossBias = 4096;  // bytes of a 128 x 16 bf16 operand: 2,048 of columns 0 to 7, then 8 to 15
 // Registers per thread: the eight softmax warps hold a whole row of scores (128), the others
 // need few. 256 * 184 + 256 * 72 = 512 * 128, the block's share at launch.
 constexpr int kCrossSoftmaxRegs = 184, kCrossOtherRegs = 72;
@@ -58,15 +59,20 @@ struct CrossFwdArgs {
   uint64_t timeout_ns;
 };
 
-template <int D>
+template <int D, int MASK>
 struct CrossFwdLayout {
   static constexpr int TILE = 128 * D * 2;
   // Query tile of each job, two staging buffers of 64 channels, the ring of key and value tiles.
   // Four ring tiles at d = 128: with three, a key tile waits for the values of two blocks before
   // (the issuer waited 0.4k cycles a block for it).
+  // With a mask of each key the room of one staging buffer (d = 128) or two ring tiles (d = 64) goes
+  // to the masks as operands: kBias bytes for the ones and for every other ring slot.
+  static constexpr bool BIAS = MASK == 2;
+  static constexpr int STAGES = D == 128 && BIAS ? 1 : 2;
+  static constexpr int NKV = D == 128 ? 4 : BIAS ? 8 : 10;
   static constexpr int STAGE_OFF = 2 * TILE;
-  static constexpr int KV_OFF = STAGE_OFF + 2 * int(kCrossBlk);
-  static constexpr int NKV = D == 128 ? 4 : 10;
+  static constexpr int BIAS_OFF = STAGE_OFF + STAGES * int(kCrossBlk);
+  static constexpr int KV_OFF = BIAS_OFF + (BIAS ? (1 + NKV / 2) * kCrossBias : 0);
   // Split keys: each job takes half of the ring as its own. (With one ring for both, the reader of
   // a tile would not see the phases of the tiles that the other job reads, and a wait by parity
   // needs every phase.)
@@ -85,7 +91,7 @@ struct CrossFwdLayout {
 template <int D, int MASK>
 __global__ void __launch_bounds__(kCrossThreads, 1)
     cross_fwd_tc_kernel(const __grid_constant__ CrossMaps maps, const __grid_constant__ CrossFwdArgs args) {
-  using Lay = CrossFwdLayout<D>;
+  using Lay = CrossFwdLayout<D, MASK>;
   constexpr int DH = D / 64;
   constexpr bool MASKED = MASK > 0;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -112,6 +118,11 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   if (warp == 14) {  // a warp whose lanes stay together: TMEM is taken and given back by whole warps
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
+  }
+  if (MASK == 2) {  // column 0 of the ones; the masks' columns 1 to 15 stay zero
+    for (uint32_t at = threadIdx.x * 16; at < uint32_t(Lay::KV_OFF - Lay::BIAS_OFF); at += kCrossThreads * 16)
+      st_shared_v4(smem_u32(smem) + Lay::BIAS_OFF + at, at < 2048u ? 0x3f80u : 0u, 0u, 0u, 0u);
+    fence_async_smem();
   }
   if (warp == 12 && lane == 0) {
     prefetch_tmap(&maps.q);
@@ -187,9 +198,12 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       // ============================================================== masked value rows to zero
       if (MASKED) {
         uint32_t e[2] = {0, 0}, blocks[2] = {0, 0};
-        // a key tile: the masks of its block go to the softmax warps, which replace masked scores, so
-        // the tile is passed on as it is. A block's place is free again: its key tile came into a
-        // ring slot that the softmax of at least kCrossWords - 1 - NKV / 2 blocks before is behind.
+        // a key tile with a mask of each key: masked rows to zero, and the mask as an operand (0 or -inf
+        // in column 0), whose product with a column of ones puts masked scores to -inf; the words
+        // themselves go to the softmax warps. (A key tile lies in every other ring slot, and has the
+        // operand's place as long as the slot.) A block's place among the words is free again: its key
+        // tile came into a ring slot that the softmax of at least kCrossWords - 1 - NKV / 2 blocks
+        // before is behind.
         auto pass = [&](int x, bool value, const uint32_t (&w)[4]) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
           if (!cross_warp_wait(&bars[Lay::KVF + s], ring.use(n) & 1, abort_flag, to)) return false;
@@ -197,9 +211,17 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
           } else {
             const uint32_t at = x * kCrossWords + (x ? blocks[1] : blocks[0]) % kCrossWords;
-            if (MASK == 2 && lane == 0) {
-              st_shared_v4(sbase + Lay::WORD_OFF + at * 16, w[0], w[1], w[2], w[3]);
-              mbar_arrive(&bars[Lay::WF + at]);
+            if (MASK == 2) {
+              zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                st_shared_v4(sbase + Lay::BIAS_OFF + (1 + (s >> 1)) * kCrossBias + (32 * j + lane) * 16,
+                             (w[j] >> lane) & 1u ? 0u : 0xff80u, 0u, 0u, 0u);
+              fence_async_smem();
+              if (lane == 0) {
+                st_shared_v4(sbase + Lay::WORD_OFF + at * 16, w[0], w[1], w[2], w[3]);
+                mbar_arrive(&bars[Lay::WF + at]);
+              }
             }
             x ? ++blocks[1] : ++blocks[0];
           }
@@ -269,7 +291,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
       const uint32_t el = elect_one(), tm = uniform(tmem);
       const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + Lay::KV_OFF, 16, 1024),
-                     v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024);
+                     v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024),
+                     ones = sdesc_plain(sbase + Lay::BIAS_OFF, 2048, 128);
       auto wait = [&](int bar, uint32_t parity) -> bool {
         return cross_warp_wait(&bars[bar], parity, abort_flag, to);
       };
@@ -338,6 +361,8 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           const uint32_t off = ((kk >> 2) * kCrossBlk + (kk & 3) * 32) >> 4;
           mma_ss_by(el, ts, qa + off, ka + off, id_s, kk > 0 ? 1u : 0u);
         }
+        if (MASK == 2)  // 1 times 0 or -inf
+          mma_ss_by(el, ts, ones, ones + (1 + ((kpos & 255u) >> 1)) * (kCrossBias >> 4), id_s, 1u);
         tc_commit_by(el, &bars[Lay::SF + x]);
         if (done) tc_commit_by(el, &bars[Lay::KVE + (kpos & 255u)]);
         if (last) tc_commit_by(el, &bars[Lay::QE + x]);
@@ -426,9 +451,9 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         }
 #pragma unroll 1
         for (int h = 0; h < DH; ++h, ++halves) {
-          const uint32_t stage = sbase + Lay::STAGE_OFF + (halves & 1) * kCrossBlk + row0 * 128;
-          // the store before the last has read this buffer
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          const uint32_t stage = sbase + Lay::STAGE_OFF + (halves % Lay::STAGES) * kCrossBlk + row0 * 128;
+          // the last store into this buffer has read it
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Lay::STAGES - 1) : "memory");
           __syncwarp();
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
@@ -488,6 +513,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       // a warp whose rows all lie past the last query has nothing to compute
       const bool idle = qt * 128 + (warp & 3) * 32 >= args.n;
       float m_run = -INFINITY, l_run = 0.f;
+      uint32_t any = MASK == 2 ? 0u : 1u;  // a key counts
       for (int k = 0; k < r.nk; ++k, ++sc) {
         if (!(ok = wwait(&bars[Lay::SF + x], sc & 1))) break;
         tc_fence_after();
@@ -503,6 +529,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           w[1] = t.y;
           w[2] = t.z;
           w[3] = t.w;
+          any |= w[0] | w[1] | w[2] | w[3];
           ++words;
         } else {
           block_words((MASKED ? len_of(it.b) : args.m) - (r.k0 + k) * 128, nullptr, lane, w);
@@ -517,8 +544,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         const bool partial = (w[0] & w[1] & w[2] & w[3]) != ~0u;
         // Without a mask of each key only the last block is partial: its scores past the keys become
         // -inf where they lie, in a short loop (the code below is fetched for every block and has to
-        // stay small: selects in registers cost the padded 53,680 pair 3%, and save 6% where every
-        // block has holes)
+        // stay small: selects in registers cost the padded 53,680 pair 3%)
         if (MASK < 2 && partial) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -538,13 +564,6 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait(v[c]);
-        if (MASK == 2 && partial) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((w[c] >> e) & 1u)) v[c][e] = 0xff800000u;
-        }
         float a[8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -604,6 +623,10 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
         m_run = m_use;
       }
       if (!ok) break;
+      if (any == 0u) {  // zeros, whatever the query holds
+        m_run = -INFINITY;
+        l_run = 0.f;
+      }
       // the row's statistics for the epilogue, which has read the last job's
       if (!(ok = wwait(&bars[Lay::LE + x], (jobs & 1) ^ 1))) break;
       st_shared_f2(sbase + Lay::STAT_OFF + (x * 128 + row) * 8, m_run * c2, l_run);

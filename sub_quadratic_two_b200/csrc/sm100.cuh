@@ -214,6 +214,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// The same without a swizzle, K-major: core matrices of 8 rows x 16 B (128 B in a piece), lbo apart
+// along K and sbo apart along the rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | uint64_t((lbo >> 4) & 0x3FFFu) << 16 |
+         uint64_t((sbo >> 4) & 0x3FFFu) << 32 | uint64_t(1) << 46;
+}
+
 // 32 lanes x 32 columns of 32-bit TMEM -> 32 registers per thread (thread = lane),
 // followed by the wait so the registers are valid on return.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {

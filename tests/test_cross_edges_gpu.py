@@ -247,3 +247,20 @@ def test_captured_training_step(cuda_ok, dtype):
         assert all(torch.equal(a, b) for a, b in zip(grads, eg))
     assert alive.shape == q.shape
     sq.poll_device_error()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,m", [(300, 200), (1, 3000)])
+def test_queries_without_states_may_hold_anything(cuda_ok, d, n, m):
+    q, k, v, _ = problem(47, 3, 2, 2, n, m, d)
+    q[1] = float("nan")
+    q[2] = float("inf")
+    mask = torch.ones(3, m, dtype=torch.bool, device="cuda")
+    mask[1:] = False
+    lens = torch.tensor([m, 0, 0], dtype=torch.int32, device="cuda")
+    keep, s = keep_of(3, m, None, mask), d ** -0.5
+    bound = bounds(q[:1], k[:1], v[:1], keep[:1], s)[0]
+    for kw in (dict(key_mask=mask), dict(kv_lens=lens), dict(key_mask=mask, kv_lens=lens)):
+        o, lse = sq.squad_cross_fwd(q, k, v, **kw)
+        assert (o[1:] == 0).all() and (lse[1:] == -float("inf")).all()
+        assert_within(o[:1], forward(q[:1], k[:1], v[:1], keep[:1], s)[0], bound, "o")
