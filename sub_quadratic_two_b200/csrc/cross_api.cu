@@ -122,12 +122,14 @@ struct FwdWs {
   size_t part_lse, total;  // parts of o first
 };
 
-// Rows per thread of the fp32 kernels (16 times as many to a tile): as many as leave one and a half
-// to two blocks for each SM, and as the tiles of a wide head leave room for.
+// Rows of the fp32 forward and dq tiles, in 16s: 32 where that leaves a block for three quarters of
+// the SMs (24 heads of 96, 300 x 300: forward 64 us with 16 rows, 54 with 32; 2 heads of 192, 2,000 x
+// 500: 95 and 75; but 2 heads of 64, 256 x 77: 8.6 and 10.7).
 int f32_rows(const squad_cross_desc* d) {
-  const long long bh = (long long)d->B * d->heads;
-  if (d->d <= 160 && bh * ((d->n + 63) / 64) >= 2 * sq::kCrossPlanSms) return 4;
-  return bh * ((d->n + 31) / 32) >= 3 * sq::kCrossPlanSms / 2 ? 2 : 1;
+  return (long long)d->B * d->heads * ((d->n + 31) / 32) * 4 >= 3 * sq::kCrossPlanSms ? 2 : 1;
+}
+sq::CrossF32Dkdv f32_dkdv(const squad_cross_desc* d) {
+  return sq::cross_f32_dkdv_plan((long long)d->B * d->kv_heads, d->heads / d->kv_heads, d->n, d->m, d->d);
 }
 
 FwdWs fwd_workspace(const squad_cross_desc* d) {
@@ -169,17 +171,38 @@ squad_status f32_cross_fwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cu
   return SQUAD_OK;
 }
 
+// dq of queries whose keys were cut into parts
+template <typename T>
+squad_status join_dq(const float* part, int splits, int B, int heads, int n, int D, T* dq, const sq::CrossStride& sdq,
+                     cudaStream_t st) {
+  const long long rows = (long long)B * heads * n;
+  sq::cross_join_grads_kernel<T><<<unsigned((rows * (D / 4) + 255) / 256), 256, 0, st>>>(part, splits, rows, n, heads, n,
+                                                                                         D, rows, dq, sdq, dq, sdq);
+  SQ_CUDA(cudaGetLastError());
+  return SQUAD_OK;
+}
+
 template <int D, int R>
-squad_status f32_cross_bwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
-  static std::atomic<bool> done_q[kMaxDevices], done_kv[kMaxDevices];
+squad_status f32_cross_dq(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
   auto dq = sq::cross_f32_dq_kernel<D, R>;
-  auto dkv = sq::cross_f32_dkdv_kernel<D, R>;
   squad_status s;
-  if ((s = allow_smem(dq, sq::F32Layout<D, R>::DQ, dev, done_q)) != SQUAD_OK) return s;
-  if ((s = allow_smem(dkv, sq::F32Layout<D, R>::DKV, dev, done_kv)) != SQUAD_OK) return s;
-  const dim3 gq(unsigned((a.n + 16 * R - 1) / (16 * R)), unsigned(a.heads), unsigned(a.B));
+  if ((s = allow_smem(dq, sq::F32Layout<D, R>::DQ, dev, done)) != SQUAD_OK) return s;
+  const dim3 gq(unsigned((a.n + 16 * R - 1) / (16 * R) * a.dq_splits), unsigned(a.heads), unsigned(a.B));
   dq<<<gq, sq::kF32Threads, sq::F32Layout<D, R>::DQ, st>>>(a);
   SQ_CUDA(cudaGetLastError());
+  if (a.dq_splits > 1 && (s = join_dq<float>(a.dq_part, a.dq_splits, a.B, a.heads, a.n, D, static_cast<float*>(a.dq),
+                                             a.sdq, st)) != SQUAD_OK)
+    return s;
+  return SQUAD_OK;
+}
+
+template <int D, int R>
+squad_status f32_cross_dkdv(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  auto dkv = sq::cross_f32_dkdv_kernel<D, R>;
+  squad_status s;
+  if ((s = allow_smem(dkv, sq::F32Layout<D, R>::DKV, dev, done)) != SQUAD_OK) return s;
   const dim3 gk(unsigned((a.m + 16 * R - 1) / (16 * R) * a.splits), unsigned(a.kv_heads), unsigned(a.B));
   dkv<<<gk, sq::kF32Threads, sq::F32Layout<D, R>::DKV, st>>>(a);
   SQ_CUDA(cudaGetLastError());
@@ -194,19 +217,22 @@ squad_status f32_cross_bwd(const sq::HostDevice& dev, const sq::CrossArgs& a, cu
   return SQUAD_OK;
 }
 
-template <int D, int R, bool BWD>
+enum F32Kernel { kF32Fwd, kF32Dq, kF32Dkdv };
+
+template <F32Kernel WHICH, int D, int R>
 squad_status f32_cross_run(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
-  return BWD ? f32_cross_bwd<D, R>(dev, a, st) : f32_cross_fwd<D, R>(dev, a, st);
+  if constexpr (WHICH == kF32Fwd) return f32_cross_fwd<D, R>(dev, a, st);
+  if constexpr (WHICH == kF32Dq) return f32_cross_dq<D, R>(dev, a, st);
+  if constexpr (WHICH == kF32Dkdv) return f32_cross_dkdv<D, R>(dev, a, st);
 }
 
-template <bool BWD>
-squad_status f32_cross(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& a, cudaStream_t st) {
-  const int r = f32_rows(d);
-#define SQ_D(N)                                                   \
-  case N:                                                         \
-    return r == 4   ? f32_cross_run<N, (N <= 160 ? 4 : 2), BWD>(dev, a, st) \
-           : r == 2 ? f32_cross_run<N, 2, BWD>(dev, a, st)        \
-                    : f32_cross_run<N, 1, BWD>(dev, a, st)
+template <F32Kernel WHICH>
+squad_status f32_cross(const sq::HostDevice& dev, int r, const sq::CrossArgs& a, cudaStream_t st) {
+#define SQ_D(N)                                                                                         \
+  case N:                                                                                               \
+    return r == 4   ? f32_cross_run<WHICH, N, (WHICH == kF32Dkdv && N <= 160 ? 4 : 2)>(dev, a, st)      \
+           : r == 2 ? f32_cross_run<WHICH, N, 2>(dev, a, st)                                            \
+                    : f32_cross_run<WHICH, N, 1>(dev, a, st)
   switch (a.d) {
     SQ_D(32);
     SQ_D(64);
@@ -293,8 +319,8 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
 // ---------------------------------------------------------------- tensor-core backward (bf16)
 
 struct BwdWs {
-  size_t part, total;  // D vector first
-  int splits;
+  size_t part, dq_part, total;  // D vector first
+  int splits, dq_splits;
 };
 
 BwdWs bwd_workspace(const squad_cross_desc* d) {
@@ -303,12 +329,16 @@ BwdWs bwd_workspace(const squad_cross_desc* d) {
   w.part = bwd_rowvec_bytes(d);
   w.total = w.part;
   const bool tc = d->dtype == SQUAD_BF16;
-  const int keys = tc ? 128 : 16 * f32_rows(d), queries = tc ? 128 : sq::kF32Cols;
-  const long long units = (long long)d->B * d->kv_heads * ((d->m + keys - 1) / keys);
-  const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + queries - 1) / queries);
-  w.splits = sq::cross_dkv_splits(units, int(tiles));
+  const long long units = (long long)d->B * d->kv_heads * ((d->m + 127) / 128);
+  const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + 127) / 128);
+  w.splits = tc ? sq::cross_dkv_splits(units, int(tiles)) : f32_dkdv(d).splits;
   const size_t rows = tc ? size_t(units) * 128 : size_t(d->B) * d->kv_heads * d->m;
   if (w.splits > 1) w.total += align256(size_t(2) * w.splits * rows * d->d * sizeof(float));
+  const int qrows = tc ? 128 : 16 * f32_rows(d), kcols = tc ? 128 : sq::kF32Cols;
+  w.dq_splits = sq::cross_dq_splits((long long)d->B * d->heads * ((d->n + qrows - 1) / qrows), (d->m + kcols - 1) / kcols,
+                                    tc);
+  w.dq_part = w.total;
+  if (w.dq_splits > 1) w.total += align256(size_t(w.dq_splits) * d->B * d->heads * d->n * d->d * sizeof(float));
   return w;
 }
 
@@ -321,9 +351,11 @@ squad_status launch_cross_bwd(const sq::HostDevice& dev, const sq::CrossBwdMaps&
   auto dkv = sq::cross_bwd_dkdv_kernel<D, MASKED>;
   if ((s = allow_smem(dq, sq::CrossDqLayout<D>::BYTES, dev, done_q)) != SQUAD_OK) return s;
   if ((s = allow_smem(dkv, sq::CrossDkvLayout<D>::BYTES, dev, done_kv)) != SQUAD_OK) return s;
-  a.items = a.B * a.heads * a.qtiles;
+  a.items = a.B * a.heads * a.qtiles * a.dq_splits;
   dq<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDqLayout<D>::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
+  if (a.dq_splits > 1 && (s = join_dq<__nv_bfloat16>(a.dq_part, a.dq_splits, a.B, a.heads, a.n, D, a.dq, a.sdq, st)) != SQUAD_OK)
+    return s;
   a.items = a.B * a.kv_heads * a.kblocks * a.splits;
   dkv<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDkvLayout<D>::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
@@ -352,6 +384,9 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.kblocks = (d->m + 127) / 128;
   const BwdWs w = bwd_workspace(d);
   a.splits = w.splits;
+  a.dq_splits = w.dq_splits;
+  a.f_dq = sq::make_fastdiv(uint32_t(a.qtiles * a.dq_splits));
+  a.f_dq_splits = sq::make_fastdiv(uint32_t(a.dq_splits));
   a.f_qtiles = sq::make_fastdiv(uint32_t(a.qtiles));
   a.f_heads = sq::make_fastdiv(uint32_t(a.heads));
   a.f_group = sq::make_fastdiv(uint32_t(a.group));
@@ -379,6 +414,7 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.dk = static_cast<__nv_bfloat16*>(c.dk);
   a.dv = static_cast<__nv_bfloat16*>(c.dv);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
+  a.dq_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.dq_part);
   a.err = dev.err;
   a.timeout_ns = sq::kWaitTimeoutNs;
   const bool masked = c.mask.lens != nullptr || c.mask.keys != nullptr;
@@ -428,7 +464,7 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
   a.part = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part_lse);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, st) : f32_cross<false>(dev, desc, a, st);
+  return desc->dtype == SQUAD_BF16 ? tc_cross_fwd(dev, desc, a, st) : f32_cross<kF32Fwd>(dev, f32_rows(desc), a, st);
 }
 
 squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
@@ -460,8 +496,12 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   const BwdWs w = bwd_workspace(desc);
   a.splits = w.splits;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
+  a.dq_splits = w.dq_splits;
+  a.dq_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.dq_part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return desc->dtype == SQUAD_BF16 ? tc_cross_bwd(dev, desc, a, workspace, st) : f32_cross<true>(dev, desc, a, st);
+  if (desc->dtype == SQUAD_BF16) return tc_cross_bwd(dev, desc, a, workspace, st);
+  if ((s = f32_cross<kF32Dq>(dev, f32_rows(desc), a, st)) != SQUAD_OK) return s;
+  return f32_cross<kF32Dkdv>(dev, f32_dkdv(desc).rows, a, st);
 }
 
 // ---------------------------------------------------------------- rotary positions

@@ -37,6 +37,9 @@ struct CrossArgs {
   // where there are several
   int splits;
   float *part, *part_lse;
+  // dq kernel: parts of the keys, and their results where there are several
+  int dq_splits;
+  float* dq_part;
 };
 
 template <typename T>

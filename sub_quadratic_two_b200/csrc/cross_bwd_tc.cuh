@@ -28,7 +28,9 @@ struct CrossBwdArgs {
   int B, heads, kv_heads, group, n, m;
   int qtiles, kblocks;
   int splits;             // dk, dv kernel: parts of a key tile's queries
-  int items;              // dq kernel: query tiles in all; dk, dv kernel: (key tile, split) units
+  int dq_splits;          // dq kernel: parts of a query tile's keys
+  int items;              // dq kernel: (query tile, part) in all; dk, dv kernel: (key tile, part) units
+  FastDiv f_dq, f_dq_splits;  // dq items of a (batch, head), of a query tile
   FastDiv f_qtiles, f_heads, f_group, f_kblocks, f_kv_heads;
   int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h;  // 1, or 0 where the map has no such extent
   CrossMask mask;
@@ -38,6 +40,7 @@ struct CrossBwdArgs {
   const float* lse;       // [B, heads, n]
   float* Drow;            // [B, heads, n]: written by the dq kernel, read by the other
   __nv_bfloat16 *dq, *dk, *dv;
+  float* dq_part;         // dq_splits > 1: [part][B, heads, n][D] fp32
   float* part;            // splits > 1: [dk, dv][split][B, kv_heads, kblocks * 128][D] fp32
   int* err;
   uint64_t timeout_ns;
@@ -121,11 +124,12 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
   const uint32_t sbase = smem_u32(smem);
 
   struct Item {
-    int b, h, hk, qt;
+    int b, h, hk, qt, sp;
   };
   auto item_of = [&](int i) -> Item {
-    const int bh = fdiv(i, args.f_qtiles), b = fdiv(bh, args.f_heads), h = bh - b * args.heads;
-    return Item{b, h, fdiv(h, args.f_group), i - bh * args.qtiles};
+    const int bh = fdiv(i, args.f_dq), b = fdiv(bh, args.f_heads), h = bh - b * args.heads;
+    const int r = i - bh * args.qtiles * args.dq_splits, qt = fdiv(r, args.f_dq_splits);
+    return Item{b, h, fdiv(h, args.f_group), qt, r - qt * args.dq_splits};
   };
   int len_b = -1, len_v = 0;
   auto len_of = [&](int b) -> int {
@@ -136,11 +140,14 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     }
     return len_v;
   };
-  // blocks of a batch row; one (all masked) where no key counts
+  // key blocks of an item of batch row b, one at least; a part short of keys runs blocks past the
+  // length (all masked), as an item does where no key counts
   auto blocks_of = [&](int b) -> int {
-    const int nb = (len_of(b) + 127) >> 7;
-    return nb > 1 ? nb : 1;
+    const int nb = (len_of(b) + 127) >> 7, per = args.dq_splits > 1 ? (nb + args.dq_splits - 1) / args.dq_splits : nb;
+    return per > 1 ? per : 1;
   };
+  // whether D is summed with dS: the item's one block holds every key
+  auto exact_d = [&](int b) -> bool { return args.dq_splits == 1 && blocks_of(b) == 1; };
   auto load = [&](uint32_t dst, const CUtensorMap* m, uint64_t* bar, int row, int h, int b) {
     mbar_arrive_expect_tx(bar, Lay::TILE);
 #pragma unroll
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         for (int k = 0; ok && k < nk; ++k) {
           const uint32_t s = e % Lay::NK;
           if (!(ok = cross_wait(&bars[Lay::KE + s], ((e / Lay::NK) & 1) ^ 1, abort_flag, to))) break;
-          load(sbase + Lay::K_OFF + s * Lay::TILE, &maps.k, &bars[Lay::KF + s], k * 128, it.hk * args.k_h, it.b * args.k_b);
+          load(sbase + Lay::K_OFF + s * Lay::TILE, &maps.k, &bars[Lay::KF + s], (it.sp * nk + k) * 128, it.hk * args.k_h, it.b * args.k_b);
           ++e;
           if (k == 0) {
             if (!(ok = cross_wait(&bars[Lay::QE], (q & 1) ^ 1, abort_flag, to))) break;
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         for (int k = 0; ok && k < nk; ++k) {
           const uint32_t s = e % Lay::NV;
           if (!(ok = cross_wait(&bars[Lay::VE + s], ((e / Lay::NV) & 1) ^ 1, abort_flag, to))) break;
-          load(sbase + Lay::V_OFF + s * Lay::TILE, &maps.v, &bars[Lay::VF + s], k * 128, it.hk * args.v_h, it.b * args.v_b);
+          load(sbase + Lay::V_OFF + s * Lay::TILE, &maps.v, &bars[Lay::VF + s], (it.sp * nk + k) * 128, it.hk * args.v_h, it.b * args.v_b);
           ++e;
           if (k == 0) {
             if (!(ok = cross_wait(&bars[Lay::DOE], (q & 1) ^ 1, abort_flag, to))) break;
@@ -216,8 +223,9 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         const int len = len_of(it.b), nk = blocks_of(it.b);
         for (int k = 0; k < nk; ++k, ++t) {
           uint32_t w[4];
-          block_words(len - k * 128,
-                      args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + k * 128, lane, w);
+          const int key = (it.sp * nk + k) * 128;
+          block_words(len - key, args.mask.keys == nullptr ? nullptr : args.mask.keys + it.b * args.mask.stride + key,
+                      lane, w);
           const uint32_t sk = t % Lay::NK, sv = t % Lay::NV;
           if (!(ok = cross_warp_wait(&bars[Lay::KF + sk], (t / Lay::NK) & 1, abort_flag, to))) break;
           zero_rows<D>(sbase + Lay::K_OFF + sk * Lay::TILE, w, lane);
@@ -357,9 +365,10 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       ++made;
       return true;
     };
-    // D of the tiles whose keys span several blocks (the others' comes with their dS)
+    // D of the tiles whose keys span several blocks (the others' comes with their dS; every part of a
+    // tile makes the same D)
     auto make_d_if = [&](int i) -> bool {
-      return i >= args.items || blocks_of(item_of(i).b) == 1 || make_d(i);
+      return i >= args.items || exact_d(item_of(i).b) || make_d(i);
     };
     ok = make_d_if(blockIdx.x);
     uint32_t job = 0;
@@ -371,12 +380,22 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
       const uint32_t t = tmem + (uint32_t(ew * 32) << 16) + 384;
       const int tok = it.qt * 128 + row;
       __nv_bfloat16* out = args.dq + it.b * args.sdq.b + it.h * args.sdq.h + (long long)tok * args.sdq.n;
+      float* part = args.dq_part +
+                    (((long long)it.sp * args.B * args.heads + (long long)it.b * args.heads + it.h) * args.n + tok) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
         __syncwarp();  // lanes part below: TMEM is read by whole warps
         tmem_ld32(t + c, v);
-        if (tok < args.n) {
+        if (args.dq_splits > 1) {
+          if (tok < args.n) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(part + c + e) = make_float4(
+                  __uint_as_float(v[e]) * args.scale, __uint_as_float(v[e + 1]) * args.scale,
+                  __uint_as_float(v[e + 2]) * args.scale, __uint_as_float(v[e + 3]) * args.scale);
+          }
+        } else if (tok < args.n) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t p[4];
@@ -403,6 +422,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
       const Item it = item_of(i);
       const int len = len_of(it.b), nk = blocks_of(it.b), tok = it.qt * 128 + row;
+      const bool exact = exact_d(it.b);
       const bool idle = it.qt * 128 + (warp & 3) * 32 >= args.n;
       // rows past the last query and rows without keys: P = 2^(s - inf) = 0
       float lse2 = INFINITY;
@@ -425,7 +445,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
           wb = g ? w.w : w.y;
         } else {
           uint32_t w[4];
-          block_words(len - k * 128, nullptr, lane, w);
+          block_words(len - (it.sp * nk + k) * 128, nullptr, lane, w);
           wa = g ? w[2] : w[0];
           wb = g ? w[3] : w[1];
         }
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
             p[e + 1] = ex2_approx(f2_hi(z));
           }
         }
-        if (k == 0 && nk > 1) {
+        if (k == 0 && !exact) {
           if (!(ok = cross_warp_wait(&bars[Lay::DF + (made & 1)], (made >> 1) & 1, abort_flag, to))) break;
           // written by this CTA's epilogue warps, ordered by the barrier (so not read as constant data)
           if (tok < args.n) Dv = *static_cast<volatile float*>(args.Drow + ((long long)it.b * args.heads + it.h) * args.n + tok);
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         }
         if (!(ok = cross_warp_wait(&bars[Lay::DPF], t & 1, abort_flag, to))) break;
         tc_fence_after();
-        if (nk == 1 && !idle) {
+        if (exact && !idle) {
           // D of the row: each half's sum of P dP, exchanged with the warp of the other half
           uint64_t acc = 0ull;
 #pragma unroll

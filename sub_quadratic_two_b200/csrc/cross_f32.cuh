@@ -9,8 +9,9 @@
 // FMAs) or 4 rows of results: the 256 threads are 4 R groups of rows x 16 of columns (or
 // channels) x S = 4 / R parts of the sum, along the channels for scores and along the 64 for
 // results. The parts of a score are joined by shuffles, those of a result once at the end.
-// Forward, 8 heads of 128, 4,096 x 1,024: 703 us with R = 1, 562 with 2, 629 with 4 (31 TFLOP/s; the
-// shared-memory passes of R = 2 take 0.4 ms of it); 1,000 x 130, 4 heads of 96: 23, 23 and 37 us.
+// The loads of a tile are not covered by the products of the one before, but by another block's.
+// Forward, 8 heads of 128, 4,096 x 1,024: 703 us with R = 1, 562 with 2 (31 TFLOP/s; the
+// shared-memory passes take 0.4 ms of it); 1,000 x 130, 4 heads of 96: 23 and 23 us.
 // Keys that do not count are zero-filled instead of read.
 #pragma once
 #include <cstdint>
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_fwd_kernel(const __grid
   }
 }
 
+// Parts of the keys as in the forward: a.dq_splits, their results in a.dq_part.
 template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_constant__ CrossArgs a) {
   using Lay = F32Layout<D, R>;
@@ -308,7 +310,8 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
   extern __shared__ __align__(16) float f32_smem[];
   float *qs = f32_smem, *dos = qs + Lay::ROWS, *ks = dos + Lay::ROWS, *vs = ks + Lay::COLS, *ps = vs + Lay::COLS,
         *keep = ps + Lay::P, *lse = keep + kF32Cols, *dd = lse + Lay::NR;
-  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = blockIdx.x * Lay::NR;
+  const int qt = blockIdx.x / a.dq_splits, sp = blockIdx.x - qt * a.dq_splits;
+  const int b = blockIdx.z, h = blockIdx.y, hk = h / a.group, i0 = qt * Lay::NR;
   const int y = threadIdx.x >> 4, x = threadIdx.x & 15, len = cross_len(a.mask, b, a.m);
   f32_load<D, LD>(qs, cross_row<float>(a.q, a.sq, b, h, i0), a.sq.n, Lay::NR, a.n - i0, nullptr);
   f32_load<D, LD>(dos, cross_row<float>(a.dout, a.sdo, b, h, i0), a.sdo.n, Lay::NR, a.n - i0, nullptr);
@@ -329,12 +332,14 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
     if (x == 0) {
       lse[y + 16 * i] = v == -INFINITY ? INFINITY : v;  // rows past the last, and rows without keys: P = 0
       dd[y + 16 * i] = t;
-      if (r < a.n) a.Drow[base + r] = t;
+      if (r < a.n && sp == 0) a.Drow[base + r] = t;
     }
   }
   const F32Thread<R> th;
   float acc[16 * Lay::NC] = {};
-  for (int j0 = 0; j0 < len; j0 += kF32Cols) {
+  const int tiles = (len + kF32Cols - 1) / kF32Cols, per = (tiles + a.dq_splits - 1) / a.dq_splits * kF32Cols;
+  const int k0 = sp * per, k1 = k0 + per < len ? k0 + per : len;
+  for (int j0 = k0; j0 < k1; j0 += kF32Cols) {
     __syncthreads();
     f32_keep(keep, kF32Cols, a.mask, b, j0, len);
     __syncthreads();
@@ -364,7 +369,8 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
   for (int i = 0; i < R; ++i) {
     const int r = i0 + th.result_row(i);
     if (r >= a.n) continue;
-    float* out = cross_row<float>(a.dq, a.sdq, b, h, r);
+    float* out = a.dq_splits > 1 ? a.dq_part + ((long long)sp * a.B * a.heads * a.n + base + r) * D
+                                 : cross_row<float>(a.dq, a.sdq, b, h, r);
 #pragma unroll
     for (int k = 0; k < Lay::NC; ++k) {
       if (D % 64 != 0 && th.c + 16 * k >= D / 4) continue;
@@ -375,10 +381,16 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
   }
 }
 
+// Blocks of the dk, dv kernel that share an SM (a tile's loads under the other's products): at
+// d = 96 the 128 registers that leaves cost nothing and 24 heads, 300 x 300 take 99 in place of 131
+// us; at d = 128 they spill.
+template <int D>
+constexpr int kF32DkdvBlocks = D <= 96 ? 2 : 1;
+
 // A block: 16 R keys and one part of the queries of their head group (blockIdx.x = key tile *
 // splits + part); with splits > 1 the parts go to a.part, [dk, dv][split][B, kv_heads, m][D].
 template <int D, int R>
-__global__ void __launch_bounds__(kF32Threads) cross_f32_dkdv_kernel(const __grid_constant__ CrossArgs a) {
+__global__ void __launch_bounds__(kF32Threads, kF32DkdvBlocks<D>) cross_f32_dkdv_kernel(const __grid_constant__ CrossArgs a) {
   using Lay = F32Layout<D, R>;
   constexpr int LD = Lay::LD;
   extern __shared__ __align__(16) float f32_smem[];

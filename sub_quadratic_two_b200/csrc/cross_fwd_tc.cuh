@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
-  if (MASK == 2) {  // column 0 of the ones; the masks' columns 1 to 15 stay zero
+  if constexpr (MASK == 2) {  // column 0 of the ones; the masks' columns 1 to 15 stay zero
     for (uint32_t at = threadIdx.x * 16; at < uint32_t(Lay::KV_OFF - Lay::BIAS_OFF); at += kCrossThreads * 16)
       st_shared_v4(smem_u32(smem) + Lay::BIAS_OFF + at, at < 2048u ? 0x3f80u : 0u, 0u, 0u, 0u);
     fence_async_smem();

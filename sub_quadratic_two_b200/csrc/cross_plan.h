@@ -99,6 +99,20 @@ SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   return r;
 }
 
+// How many parts the keys of a query tile are cut into (dq kernels): `tiles` query tiles over
+// `blocks` key blocks each. A part per idle SM, two blocks at least to a part. On the tensor cores
+// only for long keys, as in the forward's plan (backward of 24 heads of 128, whole / split: 1 query x
+// 1,024 keys 28.9 / 25.0 us, x 27,280 397 / 231; 384 x 1,024 37.2 / 41.2, x 2,048 55.1 / 53.6); a block
+// of fp32 takes longer than the join (2 heads of 64, 200 x 300: 37.2 / 35.0 us; 8 heads, 100 x 500:
+// 43.3 / 35.1, 1 x 4,096: 250 / 70).
+inline int cross_dq_splits(long long tiles, int blocks, bool tc) {
+  if (2 * tiles > kCrossPlanSms || blocks < (tc ? 8 : 4)) return 1;
+  if (tc && (long long)blocks * kCrossPlanSms < 32 * tiles) return 1;
+  long long s = kCrossPlanSms / tiles;
+  s = s < blocks / 2 ? s : blocks / 2;
+  return int(s < 64 ? s : 64);
+}
+
 // How many parts the queries of a key tile are cut into (dk, dv kernels): `units` key tiles of
 // `tiles` query tiles each over the SMs, in the time of one query tile
 // (about 1.1 us for the tensor cores at d = 128): rounds of units * s over the SMs, each
@@ -113,6 +127,37 @@ inline int cross_dkv_splits(long long units, int tiles) {
     if (s == 1 || cost < best_cost) {
       best = s;
       best_cost = cost;
+    }
+  }
+  return best;
+}
+
+// The dk, dv kernel in fp32: 16 `rows` keys to a block, and parts of the queries of a key tile.
+// The least of, in us (fitted to 12 sizes of 77 to 4,096 rows, to within a quarter): for each
+// round of the blocks over the SMs, per 64 queries (1.1 + 2.2 rows) d / 64, and two thirds of that to
+// begin and end; where two blocks share an SM (d <= 96) together one and a half times as long;
+// 2.5 and the parts' traffic where there is something to join. 16 rows and the parts of
+// the rule above in its place: 17.1 for 8.3 us at 2 heads of 64, 256 x 77; 76 for 45 at 8 of 32,
+// 1,500 x 200; 1,478 for 971 at 8 of 128, 4,096 x 1,024.
+struct CrossF32Dkdv {
+  int rows, splits;
+};
+inline CrossF32Dkdv cross_f32_dkdv_plan(long long kv_heads, int group, int n, int m, int d) {
+  const long long tiles = (long long)group * ((n + 63) / 64);
+  CrossF32Dkdv best{1, 1};
+  double best_cost = 0;
+  for (int r = 1; r <= (d <= 160 ? 4 : 2); r *= 2) {
+    const long long units = kv_heads * ((m + 16 * r - 1) / (16 * r));
+    const double step = (1.1 + 2.2 * r) * d / 64;
+    for (int s = 1; s <= 64 && s <= tiles; ++s) {
+      const long long blocks = units * s, per = d <= 96 ? 2 * kCrossPlanSms : kCrossPlanSms;
+      const double rounds = double((blocks + per - 1) / per) * (d <= 96 && blocks > kCrossPlanSms ? 1.5 : 1.0);
+      const double cost = rounds * step * (double((tiles + s - 1) / s) + 0.67) +
+                          (s > 1 ? 2.5 + 16.0 * s * double(kv_heads) * m * d / 4e6 : 0.0);
+      if (best_cost == 0 || cost < best_cost) {
+        best = CrossF32Dkdv{r, s};
+        best_cost = cost;
+      }
     }
   }
   return best;

@@ -51,6 +51,14 @@ int main() {
     const int tiles = 1 + rnd(500);
     const int s = sq::cross_dkv_splits(1 + rnd(300), tiles);
     if (s < 1 || s > tiles || s > 64) return fail("dkv splits", tiles, s, 0, 0);
+    const int units = 1 + rnd(300), blocks = 1 + rnd(400), ds = sq::cross_dq_splits(units, blocks, rnd(2));
+    if (ds < 1 || ds > 64 || (ds > 1 && (ds > blocks / 2 || ds * units > sq::kCrossPlanSms)))
+      return fail("dq splits", units, blocks, ds, 0);
+    const int d = 32 * (1 + rnd(8));
+    const sq::CrossF32Dkdv fp = sq::cross_f32_dkdv_plan((long long)B * hk, heads / hk, n, m, d);
+    if ((fp.rows != 1 && fp.rows != 2 && (fp.rows != 4 || d > 160)) || fp.splits < 1 || fp.splits > 64 ||
+        fp.splits > (long long)(heads / hk) * ((n + 63) / 64))
+      return fail("fp32 dk, dv plan", n, m, fp.rows, fp.splits);
   }
   std::printf("ok\n");
   return 0;
