@@ -6,10 +6,9 @@ from functools import lru_cache
 from typing import Optional
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _check, _check_aux, _dtype_code, load_library
-from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout, on_device, raw_stream
+from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout, first_order, on_device, raw_stream
 
 
 class SquadCrossDesc(ctypes.Structure):
@@ -185,7 +184,7 @@ class _CrossAttention(torch.autograd.Function):
         return o
 
     @staticmethod
-    @once_differentiable
+    @first_order
     def backward(ctx, dout):
         q, k, v, o, lse, kv_lens, key_mask = ctx.saved_tensors
         if not dense_enough(dout, dout.shape[3]):

@@ -128,9 +128,6 @@ struct FwdWs {
 int f32_rows(const squad_cross_desc* d) {
   return (long long)d->B * d->heads * ((d->n + 31) / 32) * 4 >= 3 * sq::kCrossPlanSms ? 2 : 1;
 }
-sq::CrossF32Dkdv f32_dkdv(const squad_cross_desc* d) {
-  return sq::cross_f32_dkdv_plan((long long)d->B * d->kv_heads, d->heads / d->kv_heads, d->n, d->m, d->d);
-}
 
 FwdWs fwd_workspace(const squad_cross_desc* d) {
   FwdWs w{};
@@ -321,6 +318,7 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
 struct BwdWs {
   size_t part, dq_part, total;  // D vector first
   int splits, dq_splits;
+  int f32_key_rows;  // of the fp32 dk, dv kernel, in 16s
 };
 
 BwdWs bwd_workspace(const squad_cross_desc* d) {
@@ -331,7 +329,14 @@ BwdWs bwd_workspace(const squad_cross_desc* d) {
   const bool tc = d->dtype == SQUAD_BF16;
   const long long units = (long long)d->B * d->kv_heads * ((d->m + 127) / 128);
   const long long tiles = (long long)(d->heads / d->kv_heads) * ((d->n + 127) / 128);
-  w.splits = tc ? sq::cross_dkv_splits(units, int(tiles)) : f32_dkdv(d).splits;
+  if (tc) {
+    w.splits = sq::cross_dkv_splits(units, int(tiles));
+  } else {
+    const sq::CrossF32Dkdv p =
+        sq::cross_f32_dkdv_plan((long long)d->B * d->kv_heads, d->heads / d->kv_heads, d->n, d->m, d->d);
+    w.splits = p.splits;
+    w.f32_key_rows = p.rows;
+  }
   const size_t rows = tc ? size_t(units) * 128 : size_t(d->B) * d->kv_heads * d->m;
   if (w.splits > 1) w.total += align256(size_t(2) * w.splits * rows * d->d * sizeof(float));
   const int qrows = tc ? 128 : 16 * f32_rows(d), kcols = tc ? 128 : sq::kF32Cols;
@@ -370,8 +375,8 @@ squad_status launch_cross_bwd(const sq::HostDevice& dev, const sq::CrossBwdMaps&
   return SQUAD_OK;
 }
 
-squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c, void* ws,
-                          cudaStream_t st) {
+squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, const sq::CrossArgs& c,
+                          const BwdWs& w, void* ws, cudaStream_t st) {
   sq::CrossBwdMaps maps;
   sq::CrossBwdArgs a{};
   a.B = d->B;
@@ -382,7 +387,6 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.m = d->m;
   a.qtiles = (d->n + 127) / 128;
   a.kblocks = (d->m + 127) / 128;
-  const BwdWs w = bwd_workspace(d);
   a.splits = w.splits;
   a.dq_splits = w.dq_splits;
   a.f_dq = sq::make_fastdiv(uint32_t(a.qtiles * a.dq_splits));
@@ -443,9 +447,9 @@ squad_status squad_cross_workspace_size(const squad_cross_desc* desc, int which,
 squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const void* k, const void* v,
                              const int* kv_lens, const unsigned char* key_mask, void* o, float* lse,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  size_t need = 0;
-  squad_status s = squad_cross_workspace_size(desc, 0, &need);
+  squad_status s = check_cross(desc);
   if (s != SQUAD_OK) return s;
+  const FwdWs w = fwd_workspace(desc);
   if (q == nullptr || k == nullptr || v == nullptr || o == nullptr) return SQUAD_ERR_INVALID_ARG;
   if (key_mask != nullptr && desc->mask_stride != 0 && desc->mask_stride < desc->m) return SQUAD_ERR_INVALID_ARG;
   for (const void* p : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse),
@@ -453,13 +457,12 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
     if (!aligned16(p)) return SQUAD_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(kv_lens) & 3u) return SQUAD_ERR_ALIGN;
   if ((s = check_cross_strides(desc, false)) != SQUAD_OK) return s;
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SQUAD_ERR_WORKSPACE;
+  if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return SQUAD_ERR_WORKSPACE;
   sq::HostDevice dev;
   if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
   sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
   a.o = o;
   a.lse = lse;
-  const FwdWs w = fwd_workspace(desc);
   a.splits = w.splits;
   a.part = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part_lse);
@@ -471,9 +474,9 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
                              const int* kv_lens, const unsigned char* key_mask, const void* o, const float* lse,
                              const void* dout, void* dq, void* dk, void* dv, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  size_t need = 0;
-  squad_status s = squad_cross_workspace_size(desc, 1, &need);
+  squad_status s = check_cross(desc);
   if (s != SQUAD_OK) return s;
+  const BwdWs w = bwd_workspace(desc);
   for (const void* p : {q, k, v, o, static_cast<const void*>(lse), dout, static_cast<const void*>(dq),
                         static_cast<const void*>(dk), static_cast<const void*>(dv)}) {
     if (p == nullptr) return SQUAD_ERR_INVALID_ARG;
@@ -482,7 +485,7 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   if (key_mask != nullptr && desc->mask_stride != 0 && desc->mask_stride < desc->m) return SQUAD_ERR_INVALID_ARG;
   if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u)) return SQUAD_ERR_ALIGN;
   if ((s = check_cross_strides(desc, true)) != SQUAD_OK) return s;
-  if (workspace == nullptr || workspace_bytes < need) return SQUAD_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < w.total) return SQUAD_ERR_WORKSPACE;
   sq::HostDevice dev;
   if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
   sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
@@ -493,15 +496,14 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   a.dk = dk;
   a.dv = dv;
   a.Drow = static_cast<float*>(workspace);
-  const BwdWs w = bwd_workspace(desc);
   a.splits = w.splits;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
   a.dq_splits = w.dq_splits;
   a.dq_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.dq_part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (desc->dtype == SQUAD_BF16) return tc_cross_bwd(dev, desc, a, workspace, st);
+  if (desc->dtype == SQUAD_BF16) return tc_cross_bwd(dev, desc, a, w, workspace, st);
   if ((s = f32_cross<kF32Dq>(dev, f32_rows(desc), a, st)) != SQUAD_OK) return s;
-  return f32_cross<kF32Dkdv>(dev, f32_dkdv(desc).rows, a, st);
+  return f32_cross<kF32Dkdv>(dev, w.f32_key_rows, a, st);
 }
 
 // ---------------------------------------------------------------- rotary positions

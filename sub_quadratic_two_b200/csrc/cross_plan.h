@@ -122,6 +122,7 @@ inline int cross_dkv_splits(long long units, int tiles) {
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= tiles && s <= 64; ++s) {
+    if (s > 1 && units * s > 8 * kCrossPlanSms) break;  // more parts only add to the join
     const double rounds = double((units * s + kCrossPlanSms - 1) / kCrossPlanSms);
     const double cost = rounds * (double((tiles + s - 1) / s) + 1.5) + (s > 1 ? 2.0 + 0.05 * double(units) * s : 0.0);
     if (s == 1 || cost < best_cost) {
@@ -151,6 +152,7 @@ inline CrossF32Dkdv cross_f32_dkdv_plan(long long kv_heads, int group, int n, in
     const double step = (1.1 + 2.2 * r) * d / 64;
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
       const long long blocks = units * s, per = d <= 96 ? 2 * kCrossPlanSms : kCrossPlanSms;
+      if (s > 1 && blocks > 4 * per) break;  // more parts only add to the join
       const double rounds = double((blocks + per - 1) / per) * (d <= 96 && blocks > kCrossPlanSms ? 1.5 : 1.0);
       const double cost = rounds * step * (double((tiles + s - 1) / s) + 0.67) +
                           (s > 1 ? 2.5 + 16.0 * s * double(kv_heads) * m * d / 4e6 : 0.0);

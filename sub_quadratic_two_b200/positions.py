@@ -40,6 +40,12 @@ def raw_stream(dev: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def first_order(backward):
+    """once_differentiable (a second differentiation raises), without its 3 us where none can follow."""
+    once = once_differentiable(backward)
+    return lambda ctx, *grads: once(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+
 def token_major(t: torch.Tensor) -> bool:
     """Whether a [B, heads, n, d] tensor lies in memory as [B, n, heads, d]."""
     return t.shape[1] > 1 and t.shape[2] > 1 and t.stride(1) < t.stride(2)
@@ -212,7 +218,7 @@ class _Rotary(torch.autograd.Function):
         return tuple(squad_rotary(xs, rot))
 
     @staticmethod
-    @once_differentiable
+    @first_order
     def backward(ctx, *grads):
         ctx.saved_tensors  # raises where the table was changed in the meantime
         out = [None] * len(grads)
