@@ -8,7 +8,7 @@ from typing import Optional
 import torch
 
 from . import _check, _check_aux, _dtype_code, load_library
-from .positions import SquadStrides, check_strided, dense_enough, empty_like_layout, first_order, on_device, raw_stream
+from .positions import SquadStrides, as_gradient, check_strided, empty_like_layout, first_order, on_device, raw_stream
 
 
 class SquadCrossDesc(ctypes.Structure):
@@ -74,23 +74,61 @@ def _kind(t: Optional[torch.Tensor]):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
 
 
-_calls = {}  # (what the checks look at, scale) -> what a call needs besides its pointers
+class _Call:
+    """What a checked call needs besides its pointers: the descriptor (None: nothing to launch) and the
+    workspace's bytes; of a forward also the backward calls that followed, by the kind of their dout."""
+    __slots__ = ("desc", "nb", "back")
+
+    def __init__(self, desc, nb):
+        self.desc, self.nb, self.back = desc, nb, {}
 
 
-def _call(tensors, kv_lens, key_mask, scale, build):
-    """The checked call of these kinds of tensors, made by build() the first time."""
-    try:
-        key = (tuple(map(_kind, tensors)), _kind(kv_lens), _kind(key_mask), scale)
-        return _calls[key]
-    except KeyError:
-        pass
-    except (AttributeError, TypeError):  # not a tensor: the checks say which
-        return build()
-    call = build()
-    if len(_calls) >= 1024:
-        _calls.clear()
-    _calls[key] = call
+_calls = {}  # (what the checks look at, scale) -> _Call
+
+
+def _keep(calls, key, call):
+    if len(calls) >= 1024:
+        calls.clear()
+    calls[key] = call
     return call
+
+
+def _fwd_call(q, k, v, scale, kv_lens, key_mask, out) -> _Call:
+    try:
+        key = (q.shape, q.stride(), q.dtype, q.device, k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(),
+               v.dtype, v.device, _kind(kv_lens), _kind(key_mask), _kind(out), scale)
+        call = _calls.get(key)
+    except (AttributeError, TypeError):  # not a tensor: the checks say which
+        key = call = None
+    if call is not None:
+        return call
+    step = _check_cross(q, k, v, kv_lens, key_mask)
+    if out is not None:
+        check_strided(("q", q), ("out", out))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    o = out if out is not None else empty_like_layout(q)
+    code = _dtype_code(q)
+    if q.numel() == 0 or k.numel() == 0:
+        call = _Call(None, 0)
+    else:
+        desc = _desc(q.shape, k.shape, code, scale, step, (q.stride(), k.stride(), v.stride(), o.stride()))
+        call = _Call(desc, _workspace(tuple(q.shape), tuple(k.shape), code, 0))
+    return _keep(_calls, key, call)
+
+
+def _bwd_call(q, k, v, o, lse, dout, scale, kv_lens, key_mask) -> _Call:
+    step = _check_cross(q, k, v, kv_lens, key_mask)
+    check_strided(("q", q), ("o", o), ("dout", dout))
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must have q's shape")
+    _check_aux(lse, q.shape[:3], torch.float32, q.device, "lse")
+    code = _dtype_code(q)
+    if q.numel() == 0 or k.numel() == 0:
+        return _Call(None, 0)
+    strides = [t.stride() for t in (q, k, v, o, dout)] + [empty_like_layout(t).stride() for t in (q, k, v)]
+    desc = _desc(q.shape, k.shape, code, scale, step, strides)
+    return _Call(desc, _workspace(tuple(q.shape), tuple(k.shape), code, 1))
 
 
 def cross_workspace_size(q: torch.Tensor, k: torch.Tensor, which: int) -> int:
@@ -109,31 +147,21 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
         with torch.cuda.stream(stream):
             return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
     scale = _scale(scale)
+    return _run_fwd(_fwd_call(q, k, v, scale, kv_lens, key_mask, out), q, k, v, kv_lens, key_mask, save, out)
 
-    def build():
-        step = _check_cross(q, k, v, kv_lens, key_mask)
-        if out is not None:
-            check_strided(("q", q), ("out", out))
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        o = out if out is not None else empty_like_layout(q)
-        code = _dtype_code(q)
-        if q.numel() == 0 or k.numel() == 0:
-            return None, 0
-        desc = _desc(q.shape, k.shape, code, scale, step, (q.stride(), k.stride(), v.stride(), o.stride()))
-        return desc, _workspace(tuple(q.shape), tuple(k.shape), code, 0)
 
-    desc, nb = _call((q, k, v, out), kv_lens, key_mask, scale, build)
+def _run_fwd(call, q, k, v, kv_lens, key_mask, save, out=None):
     o = empty_like_layout(q) if out is None else out
     lse = q.new_empty(q.shape[:3], dtype=torch.float32) if save else None
-    if desc is None:  # no query, or no key for any of them
+    if call.desc is None:  # no query, or no key for any of them
         o.zero_()
         if save:
             lse.fill_(float("-inf"))
         return o, lse
+    nb = call.nb
     ws = q.new_empty(nb, dtype=torch.uint8) if nb else None
     with on_device(q.device):
-        _check(load_library().squad_cross_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _check(load_library().squad_cross_fwd(ctypes.byref(call.desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                               _at(kv_lens), _at(key_mask), o.data_ptr(), _at(lse), _at(ws), nb,
                                               raw_stream(q.device)), "squad_cross_fwd")
     return o, lse
@@ -146,27 +174,24 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
         with torch.cuda.stream(stream):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
     scale = _scale(scale)
+    try:
+        key = (*map(_kind, (q, k, v, o, lse, dout)), _kind(kv_lens), _kind(key_mask), scale)
+        call = _calls.get(key)
+    except (AttributeError, TypeError):  # not a tensor: the checks say which
+        key = call = None
+    if call is None:
+        call = _keep(_calls, key, _bwd_call(q, k, v, o, lse, dout, scale, kv_lens, key_mask))
+    return _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask)
 
-    def build():
-        step = _check_cross(q, k, v, kv_lens, key_mask)
-        check_strided(("q", q), ("o", o), ("dout", dout))
-        if o.shape != q.shape or dout.shape != q.shape:
-            raise ValueError("o and dout must have q's shape")
-        _check_aux(lse, q.shape[:3], torch.float32, q.device, "lse")
-        code = _dtype_code(q)
-        if q.numel() == 0 or k.numel() == 0:
-            return None, 0
-        strides = [t.stride() for t in (q, k, v, o, dout)] + [empty_like_layout(t).stride() for t in (q, k, v)]
-        return (_desc(q.shape, k.shape, code, scale, step, strides),
-                _workspace(tuple(q.shape), tuple(k.shape), code, 1))
 
-    desc, nb = _call((q, k, v, o, lse, dout), kv_lens, key_mask, scale, build)
+def _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask):
     dq, dk, dv = empty_like_layout(q), empty_like_layout(k), empty_like_layout(v)
-    if desc is None:
+    if call.desc is None:
         return dq.zero_(), dk.zero_(), dv.zero_()
+    nb = call.nb
     ws = q.new_empty(nb, dtype=torch.uint8)
     with on_device(q.device):
-        _check(load_library().squad_cross_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _check(load_library().squad_cross_bwd(ctypes.byref(call.desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                               _at(kv_lens), _at(key_mask), o.data_ptr(), lse.data_ptr(),
                                               dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                               ws.data_ptr(), nb, raw_stream(q.device)), "squad_cross_bwd")
@@ -176,20 +201,21 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
 class _CrossAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, scale, kv_lens, key_mask):
-        need = any(ctx.needs_input_grad[:3])
-        o, lse = squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save=need)
-        if need:
-            ctx.save_for_backward(q, k, v, o, lse, kv_lens, key_mask)
-        ctx.scale = scale
+        call = _fwd_call(q, k, v, scale, kv_lens, key_mask, None)
+        o, lse = _run_fwd(call, q, k, v, kv_lens, key_mask, True)
+        ctx.save_for_backward(q, k, v, o, lse, kv_lens, key_mask)
+        ctx.scale, ctx.call = scale, call
         return o
 
     @staticmethod
     @first_order
     def backward(ctx, dout):
         q, k, v, o, lse, kv_lens, key_mask = ctx.saved_tensors
-        if not dense_enough(dout, dout.shape[3]):
-            dout = dout.contiguous()
-        return squad_cross_bwd(q, k, v, o, lse, dout, ctx.scale, kv_lens, key_mask) + (None, None, None)
+        dout, calls = as_gradient(dout), ctx.call.back
+        # q, k, v and the masks are the forward's, o and lse lie as it made them: dout alone may differ
+        kind = _kind(dout)
+        call = calls.get(kind) or _keep(calls, kind, _bwd_call(q, k, v, o, lse, dout, ctx.scale, kv_lens, key_mask))
+        return _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask) + (None, None, None)
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
@@ -205,5 +231,5 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Op
     autograd to the stream of that graph, outside the capture, and the capture fails.
     """
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        return _CrossAttention.apply(q, k, v, scale, kv_lens, key_mask)
+        return _CrossAttention.apply(q, k, v, _scale(scale), kv_lens, key_mask)
     return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save=False)[0]

@@ -74,12 +74,15 @@ def check_strided(*named):
     _dtype_code(ref)
 
 
-def dense_enough(t: torch.Tensor, rows_apart: int) -> bool:
-    """Whether the kernels take a gradient as it lies: channels contiguous, rows apart, 16-byte steps."""
-    unit = 16 // t.element_size()
-    if t.data_ptr() % 16 or (t.shape[3] > 1 and t.stride(3) != 1):
-        return False
-    return all(size <= 1 or (step >= rows_apart and step % unit == 0) for size, step in zip(t.shape[:3], t.stride()[:3]))
+def as_gradient(t: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient as the kernels take it: as it lies where its channels are contiguous, its rows
+    apart and its steps whole 16 bytes, else copied."""
+    if t.is_contiguous():
+        return t if t.data_ptr() % 16 == 0 else t.clone()
+    d, unit = t.shape[3], 16 // t.element_size()
+    fits = t.data_ptr() % 16 == 0 and (d <= 1 or t.stride(3) == 1) and all(
+        size <= 1 or (step >= d and step % unit == 0) for size, step in zip(t.shape[:3], t.stride()[:3]))
+    return t if fits else t.contiguous()
 
 
 def default_axes(d: int) -> Tuple[int, int, int]:
@@ -221,15 +224,15 @@ class _Rotary(torch.autograd.Function):
     @first_order
     def backward(ctx, *grads):
         ctx.saved_tensors  # raises where the table was changed in the meantime
-        out = [None] * len(grads)
         take = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[1 + i]]
+        out = [None] * len(grads)
         if take:
-            gs = [grads[i] if dense_enough(grads[i], grads[i].shape[3]) else grads[i].contiguous() for i in take]
+            gs = [as_gradient(grads[i]) for i in take]
             ys = []
             for i, g in zip(take, gs):
                 B, h, n, d = g.shape
                 ys.append(g.new_empty_strided((B, h, n, d), (n * h * d, d, h * d, 1)) if ctx.token_major[i]
-                          else g.new_empty((B, h, n, d)))
+                          else g.new_empty(g.shape))
             for i, y in zip(take, squad_rotary(gs, ctx.rot, inverse=True, out=ys)):
                 out[i] = y
         return (None, *out)
