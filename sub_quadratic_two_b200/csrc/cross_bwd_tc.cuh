@@ -9,6 +9,10 @@
 // [n, d] per 128 keys) would have to be added in memory: at m = 512 four times the bytes of dQ
 // in fp32 through L2, more than the two products cost.
 //
+// Measured at 27,280 x 512, 24 heads of 128: dQ 250 us, dK and dV 268 us and 15 to join their
+// parts (tensor pipe 54% and 68% busy); together 1,130 TFLOP/s of
+// the seven products, 800 of the five.
+//
 // Rounding: P and dS to bf16 before the products that read them (the tensor core's operand
 // type); D, the statistics and the accumulators in fp32; each gradient once at the end.
 #pragma once
