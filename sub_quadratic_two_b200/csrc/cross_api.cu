@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "squad.h"
 #include "cross_bwd_tc.cuh"
@@ -34,14 +35,27 @@ size_t elem_size(int dtype) { return dtype == SQUAD_BF16 ? 2 : 4; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Strides a tensor of extents B x h x n may have: multiples of 16 bytes and not negative;
-// rows at least d apart, so that no two rows overlap; a stride of an extent of 1 is not
-// looked at. broadcast: batch and head strides of 0 are allowed (inputs).
+// rows at least d apart; a stride of an extent of 1 is not looked at. broadcast (inputs): batch and
+// head strides of 0 are allowed. Else (outputs) no two rows may overlap: the strides in ascending
+// order each step over all that the smaller ones reach.
 bool stride_ok(const squad_strides& s, int B, int h, int n, int d, size_t elem, bool broadcast) {
   const long long unit = 16 / (long long)elem;
   const long long lo = broadcast ? 0 : d;
   if (n > 1 && (s.n < d || s.n % unit != 0 || s.n >= (1ll << 36))) return false;
   if (h > 1 && (s.h < lo || s.h % unit != 0 || s.h >= (1ll << 36))) return false;
   if (B > 1 && (s.b < lo || s.b % unit != 0 || s.b >= (1ll << 36))) return false;
+  if (broadcast) return true;
+  long long step[3] = {n > 1 ? s.n : 0, h > 1 ? s.h : 0, B > 1 ? s.b : 0}, size[3] = {n, h, B}, reach = d;
+  for (int i = 0; i < 3; ++i) {
+    int at = i;
+    for (int j = i + 1; j < 3; ++j)
+      if (step[j] < step[at]) at = j;
+    std::swap(step[i], step[at]);
+    std::swap(size[i], size[at]);
+    if (size[i] <= 1) continue;
+    if (step[i] < reach) return false;
+    reach += (size[i] - 1) * step[i];
+  }
   return true;
 }
 

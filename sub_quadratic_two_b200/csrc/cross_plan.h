@@ -115,16 +115,17 @@ inline int cross_dq_splits(long long tiles, int blocks, bool tc) {
 
 // How many parts the queries of a key tile are cut into (dk, dv kernels): `units` key tiles of
 // `tiles` query tiles each over the SMs, in the time of one query tile
-// (about 1.1 us for the tensor cores at d = 128): rounds of units * s over the SMs, each
-// ceil(tiles / s) tiles and 1.5 to fill and drain, plus, for s > 1, the join kernel (2) and its
-// traffic (0.05 for each part of 128 keys).
+// (1.2 to 1.8 us on the tensor cores at d = 128): rounds of units * s over the SMs, each
+// ceil(tiles / s) tiles and 1.5 to fill and drain, plus, for s > 1, the join kernel (1.6) and its
+// traffic (0.033 for each part of 128 keys). 4 x 8 heads of 128, 2,048 x 226: 31.6 us whole, 29.3 in
+// two parts; 3 x 8 heads (4) of 64, 500 x 130: 15.2 and 12.7 in three.
 inline int cross_dkv_splits(long long units, int tiles) {
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= tiles && s <= 64; ++s) {
     if (s > 1 && units * s > 8 * kCrossPlanSms) break;  // more parts only add to the join
     const double rounds = double((units * s + kCrossPlanSms - 1) / kCrossPlanSms);
-    const double cost = rounds * (double((tiles + s - 1) / s) + 1.5) + (s > 1 ? 2.0 + 0.05 * double(units) * s : 0.0);
+    const double cost = rounds * (double((tiles + s - 1) / s) + 1.5) + (s > 1 ? 1.6 + 0.033 * double(units) * s : 0.0);
     if (s == 1 || cost < best_cost) {
       best = s;
       best_cost = cost;

@@ -264,3 +264,14 @@ def test_queries_without_states_may_hold_anything(cuda_ok, d, n, m):
         o, lse = sq.squad_cross_fwd(q, k, v, **kw)
         assert (o[1:] == 0).all() and (lse[1:] == -float("inf")).all()
         assert_within(o[:1], forward(q[:1], k[:1], v[:1], keep[:1], s)[0], bound, "o")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_outputs_of_any_order_of_axes(cuda_ok, dtype):
+    # an output whose tokens are the slowest axis and batch rows the fastest is written; one whose rows overlap is not
+    q, k, v, _ = problem(48, 2, 4, 2, 10, 20, 64, dtype)
+    want, _ = sq.squad_cross_fwd(q, k, v)
+    out = torch.empty(10, 4, 2, 64, device="cuda", dtype=dtype).permute(2, 1, 0, 3)
+    assert torch.equal(sq.squad_cross_fwd(q, k, v, out=out)[0], want)
+    with pytest.raises(sq.SquadError):
+        sq.squad_cross_fwd(q, k, v, out=torch.empty(2048 * 4, device="cuda", dtype=dtype).as_strided(q.shape, (1024, 64, 64, 1)))

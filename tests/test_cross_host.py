@@ -50,6 +50,9 @@ def bwd(lib, desc, o=FAKE, lse=FAKE, dout=FAKE, dq=FAKE, dk=FAKE, dv=FAKE, ws=FA
     (dict(q=SquadStrides(4 * 10 * 68, 10 * 68, 68)), ALIGN),       # rows 136 bytes apart
     (dict(k=SquadStrides(-8, 20 * 64, 64)), ALIGN),
     (dict(o=SquadStrides(0, 10 * 64, 64)), ALIGN),                 # an output may not be broadcast
+    (dict(o=SquadStrides(4 * 10 * 64, 64, 64)), ALIGN),            # nor may its heads overlap
+    (dict(o=SquadStrides(64, 64, 8 * 64)), ALIGN),                 # nor its batch rows
+    (dict(o=SquadStrides(3 * 10 * 64, 10 * 64, 64)), ALIGN),
     (dict(q=SquadStrides(4 * 10 * 64, 10 * 64, 0)), ALIGN),
 ])
 def test_descriptor_errors(lib, kw, code):
