@@ -105,20 +105,30 @@ class Rotary:
     pairing: str = "adjacent"
 
     def __post_init__(self):
-        object.__setattr__(self, "grid", tuple(self.grid))
-        object.__setattr__(self, "axes", tuple(self.axes))
-        if len(self.grid) != 3 or len(self.axes) != 3 or min(self.grid) < 1 or min(self.axes) < 0:
+        grid, axes, t = tuple(self.grid), tuple(self.axes), self.table
+        object.__setattr__(self, "grid", grid)
+        object.__setattr__(self, "axes", axes)
+        if isinstance(t, torch.Tensor):  # plans are often made anew around a table: the same checks once
+            key = (grid, axes, self.pairing, t.shape, t.stride(), t.dtype)
+            if key in _plans:
+                return
+        if len(grid) != 3 or len(axes) != 3 or min(grid) < 1 or min(axes) < 0:
             raise ValueError("grid and axes are (time, height, width): positive sizes, channels of each")
-        if any(c % 2 for c in self.axes):
+        if any(c % 2 for c in axes):
             raise ValueError("axes must be even: channels turn in pairs")
         if self.pairing not in PAIRINGS:
             raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
-        t = self.table
-        rows = sum(size * (c // 2) for size, c in zip(self.grid, self.axes))
+        rows = sum(size * (c // 2) for size, c in zip(grid, axes))
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (rows, 2):
             raise ValueError(f"table must be float32 of shape {(rows, 2)}")
         if not t.is_contiguous():
             raise ValueError("table must be contiguous")
+        if len(_plans) >= 1024:
+            _plans.clear()
+        _plans.add(key)
+
+
+_plans = set()  # what the checks of a plan look at, of plans that passed
 
 
 def rotary_plan(grid: Sequence[int], d: int, axes: Optional[Sequence[int]] = None, theta: float = 10000.0,
@@ -167,6 +177,8 @@ def _rotary_call(xs, rot: Rotary, inverse: bool, ys):
     check_strided(("xs[0]", ref), *[(f"out[{i}]", y) for i, y in enumerate(ys)])
     if any(x.shape != y.shape for x, y in zip(xs, ys)):
         raise ValueError("out must hold one tensor of each input's shape")
+    if any(x.numel() == 0 for x in xs):
+        return None
     desc = SquadRotaryDesc(B, d, *rot.grid, *rot.axes, _dtype_code(ref), PAIRINGS[rot.pairing], int(inverse))
     return (desc, c, (ctypes.c_int * c)(*[x.shape[1] for x in xs]),
             (SquadStrides * c)(*[SquadStrides(*x.stride()[:3]) for x in xs]),
@@ -183,23 +195,23 @@ def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_rotary(xs, rot, inverse, out)
-    if out is None:
-        ys = [x.new_empty(x.shape) for x in xs]
-    else:
-        ys = list(out)
     if not xs:
         raise ValueError("one or two tensors")
-    ref = xs[0]
-    key = (tuple([(x.shape, x.stride(), x.dtype, x.device) for x in xs]),
-           tuple([(y.shape, y.stride(), y.dtype, y.device) for y in ys]),
+    # (empty_like is the shortest way to a contiguous tensor: 1.3 us where new_empty takes 2.4)
+    ys = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs] if out is None else list(out)
+    ref, last = xs[0], xs[-1]
+    # outputs made here follow from the inputs
+    key = (len(xs), ref.shape, ref.stride(), ref.dtype, ref.device, last.shape, last.stride(), last.dtype, last.device,
+           None if out is None else tuple([(y.shape, y.stride(), y.dtype, y.device) for y in ys]),
            rot.grid, rot.axes, rot.pairing, rot.table.device, inverse)
-    call = _calls.get(key)
-    if call is None:
+    try:
+        call = _calls[key]
+    except KeyError:
         call = _rotary_call(xs, rot, inverse, ys)
         if len(_calls) >= 1024:
             _calls.clear()
         _calls[key] = call
-    if any([x.numel() == 0 for x in xs]):
+    if call is None:
         full = [i for i, x in enumerate(xs) if x.numel()]
         if full:  # one of the two has no heads
             squad_rotary([xs[i] for i in full], rot, inverse, [ys[i] for i in full])
