@@ -335,7 +335,7 @@ squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int
  * [B, n, heads, d] memory is as good as head-major. Pointers and strides (of
  * extents above 1) are multiples of 16 bytes; batch and head strides of inputs may
  * be 0 (broadcast). scale <= 0 selects 1/sqrt(d). lse [B, heads, n] fp32, contiguous.
- * Outputs overlap neither each other nor an input.
+ * No two rows of an output overlap (SQUAD_ERR_ALIGN), nor an output and another or an input.
  * Limits (SQUAD_ERR_UNSUPPORTED): bf16 d in {64, 128}; f32 d a multiple of 32,
  * d <= 256; B and heads <= 65535. */
 typedef struct {
