@@ -14,8 +14,9 @@
 //   warp 15         TMA loads of query tiles: the next item's as soon as a job's last scores are made
 //   warp 13         issues every tcgen05.mma (the whole warp runs the loop, one lane's count)
 //   warp 14         masks: zeroes the masked rows of value tiles before they are used (what lies there
-//                   may be NaN or infinite, and P = 0 times NaN is NaN); with a mask of each key those
-//                   of key tiles too, and hands the mask to the tensor core as an operand
+//                   may be NaN or infinite, and P = 0 times NaN is NaN): those past a length, or, with
+//                   a mask of each key, of every tile, key tiles too, and hands the mask to the
+//                   tensor core as an operand
 // TMEM (512 columns): S of job x at [128x, 128x+128), O at [256 + D x, ...). P overwrites S in
 // place as packed bf16.
 // The order of the products is S0(0) S1(0) | PV0(0) S0(1) | PV1(0) S1(1) | ...: the jobs take
@@ -169,27 +170,30 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       // ============================================================== key and value loads
       if (lane == 0) {
         uint32_t e[2] = {0, 0};
-        auto load = [&](int x, const CUtensorMap* m, int row, int h, int b) -> bool {
+        // cut: a value tile with rows past a length, which the mask warp passes on
+        auto load = [&](int x, const CUtensorMap* m, int row, int h, int b, bool cut) -> bool {
           const uint32_t n = x ? e[1] : e[0], s = ring.slot(x, n);
           if (!cross_wait(&bars[Lay::KVE + s], (ring.use(n) & 1) ^ 1, abort_flag, to)) return false;
-          mbar_arrive_expect_tx(&bars[Lay::KVF + s], Lay::TILE);
+          uint64_t* full = &bars[(MASK == 1 && cut ? Lay::RDY : Lay::KVF) + s];
+          mbar_arrive_expect_tx(full, Lay::TILE);
 #pragma unroll
           for (int c = 0; c < DH; ++c)
-            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, &bars[Lay::KVF + s], c * 64, row, h, b);
+            tma_load_4d(sbase + Lay::KV_OFF + s * Lay::TILE + c * kCrossBlk, m, full, c * 64, row, h, b);
           x ? ++e[1] : ++e[0];
           return true;
         };
         bool ok = true;
         for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
           const CrossItem it = cross_item(plan, args.heads, i);
-          const CrossRange r = cross_range(plan, len_of(it.b), it.sp[0]);
+          const int len = len_of(it.b);
+          const CrossRange r = cross_range(plan, len, it.sp[0]);
           const int kh = it.hk * args.k_h, kb = it.b * args.k_b, vh = it.hk * args.v_h, vb = it.b * args.v_b;
           // values of block k - 1, then keys of block k
           for (int k = 0; ok && k <= r.nk; ++k)
             for (int x = 0; ok && x < ring.count; ++x) {
               const int row = (r.k0 + x * r.nk + k) * 128;
-              if (k > 0) ok = load(x, &maps.v, row - 128, vh, vb);
-              if (ok && k < r.nk) ok = load(x, &maps.k, row, kh, kb);
+              if (k > 0) ok = load(x, &maps.v, row - 128, vh, vb, row > len);
+              if (ok && k < r.nk) ok = load(x, &maps.k, row, kh, kb, false);
             }
         }
         // let every issued load land before the CTA may exit
@@ -201,7 +205,41 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       }
     } else if (warp == 14) {
       // ============================================================== masked value rows to zero
-      if (MASKED) {
+      if (MASK == 1) {
+        // Only the value tiles that a length cuts, in the order of their products: their loads arrive
+        // here (RDY), and this warp's arrival stands for the load's at the issuer (KVF). The other tiles
+        // go from the loads to the issuer. (Passing every tile on cost 53,680 x 128 with a length 166 us
+        // in place of 142, the pair of 512 and 126 states 524 in place of 508: this warp's code is fetched
+        // beside that of the softmax warps.)
+        uint32_t e[2] = {0, 0}, phase = 0;  // bit s: parity of slot s' cut tiles
+        bool ok = true;
+#pragma unroll 1
+        for (int i = blockIdx.x; ok && i < plan.items; i += gridDim.x) {
+          const CrossItem it = cross_item(plan, args.heads, i);
+          const int len = len_of(it.b);
+          const CrossRange r = cross_range(plan, len, it.sp[0]);
+          const int cut = len >> 7;  // the first such block; key block k of job x is r.k0 + x nk + k
+#pragma unroll 1
+          for (int k = cut - (r.k0 + (ring.count - 1) * r.nk) > 0 ? cut - (r.k0 + (ring.count - 1) * r.nk) : 0;
+               ok && k < r.nk; ++k)
+#pragma unroll 1
+            for (int x = 0; ok && x < ring.count; ++x) {
+              const int block = r.k0 + x * r.nk + k;
+              if (block < cut) continue;
+              // a ring holds K(0) V(0) K(1) V(1) ... of an item
+              const uint32_t s = ring.slot(x, (x ? e[1] : e[0]) + 2 * k + 1);
+              if (!(ok = cross_warp_wait(&bars[Lay::RDY + s], (phase >> s) & 1u, abort_flag, to))) break;
+              phase ^= 1u << s;
+              uint32_t w[4];
+              block_words(len - block * 128, nullptr, lane, w);
+              zero_rows<D, true>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[Lay::KVF + s]);
+            }
+          e[0] += 2 * r.nk;
+          e[1] += 2 * r.nk;
+        }
+      } else if (MASK == 2) {
         uint32_t e[2] = {0, 0}, blocks[2] = {0, 0};
         // a key tile with a mask of each key: masked rows to zero, and the mask as an operand (0 or -inf
         // in column 0), whose product with a column of ones puts masked scores to -inf; the words
@@ -216,17 +254,15 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
             zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
           } else {
             const uint32_t at = x * kCrossWords + (x ? blocks[1] : blocks[0]) % kCrossWords;
-            if (MASK == 2) {
-              zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
+            zero_rows<D>(sbase + Lay::KV_OFF + s * Lay::TILE, w, lane);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                st_shared_v4(sbase + Lay::BIAS_OFF + (1 + (s >> 1)) * kCrossBias + (32 * j + lane) * 16,
-                             (w[j] >> lane) & 1u ? 0u : 0xff80u, 0u, 0u, 0u);
-              fence_async_smem();
-              if (lane == 0) {
-                st_shared_v4(sbase + Lay::WORD_OFF + at * 16, w[0], w[1], w[2], w[3]);
-                mbar_arrive(&bars[Lay::WF + at]);
-              }
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4(sbase + Lay::BIAS_OFF + (1 + (s >> 1)) * kCrossBias + (32 * j + lane) * 16,
+                           (w[j] >> lane) & 1u ? 0u : 0xff80u, 0u, 0u, 0u);
+            fence_async_smem();
+            if (lane == 0) {
+              st_shared_v4(sbase + Lay::WORD_OFF + at * 16, w[0], w[1], w[2], w[3]);
+              mbar_arrive(&bars[Lay::WF + at]);
             }
             x ? ++blocks[1] : ++blocks[0];
           }
@@ -240,7 +276,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
           const CrossItem it = cross_item(plan, args.heads, i);
           const int len = len_of(it.b);
           const CrossRange r = cross_range(plan, len, it.sp[0]);
-          const unsigned char* keys = MASK < 2 ? nullptr : args.mask.keys + it.b * args.mask.stride;
+          const unsigned char* keys = args.mask.keys + it.b * args.mask.stride;
           uint32_t last[2][4] = {};  // masks of each job's block k - 1, for its values
           for (int k = 0; ok && k <= r.nk; ++k)
 #pragma unroll
@@ -248,7 +284,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
               if (!ok || x >= ring.count) continue;
               const int row = (r.k0 + x * r.nk + k) * 128;
               uint32_t w[4] = {0u, 0u, 0u, 0u};
-              if (k < r.nk) block_words(len - row, keys == nullptr ? nullptr : keys + row, lane, w);
+              if (k < r.nk) block_words(len - row, keys + row, lane, w);
               if (k > 0) ok = pass(x, true, last[x]);
               if (ok && k < r.nk) ok = pass(x, false, w);
 #pragma unroll
@@ -293,7 +329,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       // ============================================================== MMA issuer
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
-      constexpr int FULL = MASKED ? Lay::RDY : Lay::KVF;
+      constexpr int FULL = MASK == 2 ? Lay::RDY : Lay::KVF;
       const uint32_t el = elect_one(), tm = uniform(tmem);
       const uint64_t q0 = sdesc_sw128(sbase, 16, 1024), k0 = sdesc_sw128(sbase + Lay::KV_OFF, 16, 1024),
                      v0 = sdesc_sw128(sbase + Lay::KV_OFF, kCrossBlk, 1024),

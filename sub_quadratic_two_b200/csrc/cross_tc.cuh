@@ -176,14 +176,15 @@ __device__ __forceinline__ void tc_commit_by(uint32_t elected, uint64_t* bar) {
 }
 
 // Zeroes the rows of a 128-row tile whose bit is not set, for the tensor core (one warp).
-template <int D>
+// ROLLED: short code, for tiles that come to it rarely.
+template <int D, bool ROLLED = false>
 __device__ __forceinline__ void zero_rows(uint32_t tile, const uint32_t (&w)[4], int lane) {
   if ((w[0] & w[1] & w[2] & w[3]) == ~0u) return;
-#pragma unroll
+#pragma unroll(ROLLED ? 1 : 4)
   for (int j = 0; j < 4; ++j) {
-    if ((w[j] >> lane) & 1u) continue;
+    if (((j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3]) >> lane) & 1u) continue;
     const uint32_t row = tile + (32 * j + lane) * 128;
-#pragma unroll
+#pragma unroll(ROLLED ? 1 : D / 64)
     for (int c = 0; c < D / 64; ++c)
 #pragma unroll
       for (int z = 0; z < 8; ++z) st_shared_v4(row + c * kCrossBlk + ((z ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
