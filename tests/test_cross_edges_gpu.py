@@ -275,3 +275,15 @@ def test_outputs_of_any_order_of_axes(cuda_ok, dtype):
     assert torch.equal(sq.squad_cross_fwd(q, k, v, out=out)[0], want)
     with pytest.raises(sq.SquadError):
         sq.squad_cross_fwd(q, k, v, out=torch.empty(2048 * 4, device="cuda", dtype=dtype).as_strided(q.shape, (1024, 64, 64, 1)))
+
+
+@pytest.mark.parametrize("B,h,n,m,d", [(6, 16, 1300, 600, 64), (6, 16, 1300, 600, 128), (7, 2, 90, 6000, 128), (7, 2, 90, 6000, 64)])
+def test_lengths_of_every_kind_in_turn(cuda_ok, B, h, n, m, d):
+    # many items to an SM whose lengths end inside blocks, at their ends and before the first, and parts of the
+    # keys that lie behind a length
+    q, k, v, do = problem(49, B, h, h, n, m, d)
+    for i in range(3):
+        gen = torch.Generator().manual_seed(50 + i)
+        lens = torch.randint(0, m + 1, (B,), generator=gen)
+        lens[i], lens[i + 1], lens[i + 2] = 0, 128 * (m // 256), 1
+        check(q, k, v, do, kv_lens=lens.int().cuda(), backward_too=i == 0)
