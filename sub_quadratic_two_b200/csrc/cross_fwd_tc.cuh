@@ -72,7 +72,7 @@ struct CrossFwdLayout {
   // Four ring tiles at d = 128: with three, a key tile waits for the values of two blocks before
   // (the issuer waited 0.4k cycles a block for it).
   // With a mask of each key the room of one staging buffer (d = 128) or two ring tiles (d = 64) goes
-  // to the masks as operands: kBias bytes for the ones and for every other ring slot.
+  // to the masks as operands: kCrossBias bytes for the ones and for every other ring slot.
   static constexpr bool BIAS = MASK == 2;
   static constexpr int STAGES = D == 128 && BIAS ? 1 : 2;
   static constexpr int NKV = D == 128 ? 4 : BIAS ? 8 : 10;
@@ -87,7 +87,8 @@ struct CrossFwdLayout {
   static constexpr int WORD_OFF = STAT_OFF + 2 * 128 * 8;  // masks of eight blocks of each ring
   static constexpr int BAR_OFF = WORD_OFF + 2 * kCrossWords * 16;
   static constexpr int QF = 0, QE = QF + 2, KVF = QE + 2, KVE = KVF + NKV, RDY = KVE + NKV, SF = RDY + NKV, PF = SF + 2,
-                       OF = PF + 2, OE = OF + 2, LF = OE + 2, LE = LF + 2, WF = LE + 2, DRAIN = WF + 2 * kCrossWords, NBAR = DRAIN + 1;
+                       OF = PF + 2, OE = OF + 2, LF = OE + 2, LE = LF + 2, WF = LE + 2, DRAIN = WF + 2 * kCrossWords,
+                       NBAR = DRAIN + 1;
   static constexpr int BYTES = BAR_OFF + NBAR * 8 + 16;  // + TMEM holder, abort flag
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -558,9 +559,10 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       for (int k = 0; k < r.nk; ++k, ++sc) {
         if (!(ok = wwait(&bars[Lay::SF + x], sc & 1))) break;
         tc_fence_after();
-        // Which keys count: all below the length, or what the mask warp says. The mask warp wrote them before
-        // it passed the key tile on, so they are there by now, and the phase is the block's own: its
-        // place is taken again eight blocks later, which this job's products hold back.
+        // Which keys count: all below the length; with a mask of each key the scores have it already, and
+        // its words tell whether the job has a key at all. The mask warp wrote them before it passed
+        // the key tile on, so they are there by now, and the phase is the block's own: its place is
+        // taken again eight blocks later, which this job's products hold back.
         uint32_t w[4];
         if (MASK == 2) {
           const uint32_t at = (ring.count == 2 ? x * kCrossWords : 0u) + words % kCrossWords;
