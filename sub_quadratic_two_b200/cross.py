@@ -76,20 +76,20 @@ def _kind(t: Optional[torch.Tensor]):
 
 class _Call:
     """What a checked call needs besides its pointers: the descriptor (None: nothing to launch) and the
-    workspace's bytes; of a forward also the backward calls that followed, by the kind of their dout."""
-    __slots__ = ("desc", "nb", "back")
+    workspace's bytes."""
+    __slots__ = ("desc", "nb")
 
     def __init__(self, desc, nb):
-        self.desc, self.nb, self.back = desc, nb, {}
+        self.desc, self.nb = desc, nb
 
 
 _calls = {}  # (what the checks look at, scale) -> _Call
 
 
-def _keep(calls, key, call):
-    if len(calls) >= 1024:
-        calls.clear()
-    calls[key] = call
+def _keep(key, call):
+    if len(_calls) >= 1024:
+        _calls.clear()
+    _calls[key] = call
     return call
 
 
@@ -114,10 +114,21 @@ def _fwd_call(q, k, v, scale, kv_lens, key_mask, out) -> _Call:
     else:
         desc = _desc(q.shape, k.shape, code, scale, step, (q.stride(), k.stride(), v.stride(), o.stride()))
         call = _Call(desc, _workspace(tuple(q.shape), tuple(k.shape), code, 0))
-    return _keep(_calls, key, call)
+    return _keep(key, call)
 
 
 def _bwd_call(q, k, v, o, lse, dout, scale, kv_lens, key_mask) -> _Call:
+    try:
+        key = (q.shape, q.stride(), q.dtype, q.device, k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(),
+               v.dtype, v.device, o.shape, o.stride(), o.dtype, o.device, lse.shape, lse.stride(), lse.dtype,
+               lse.device, dout.shape, dout.stride(), dout.dtype, dout.device, _kind(kv_lens), _kind(key_mask), scale)
+        call = _calls.get(key)
+    except (AttributeError, TypeError):  # not a tensor: the checks say which
+        key = call = None
+    return call or _keep(key, _checked_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask))
+
+
+def _checked_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask) -> _Call:
     step = _check_cross(q, k, v, kv_lens, key_mask)
     check_strided(("q", q), ("o", o), ("dout", dout))
     if o.shape != q.shape or dout.shape != q.shape:
@@ -173,14 +184,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
     if stream is not None:
         with torch.cuda.stream(stream):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
-    scale = _scale(scale)
-    try:
-        key = (*map(_kind, (q, k, v, o, lse, dout)), _kind(kv_lens), _kind(key_mask), scale)
-        call = _calls.get(key)
-    except (AttributeError, TypeError):  # not a tensor: the checks say which
-        key = call = None
-    if call is None:
-        call = _keep(_calls, key, _bwd_call(q, k, v, o, lse, dout, scale, kv_lens, key_mask))
+    call = _bwd_call(q, k, v, o, lse, dout, _scale(scale), kv_lens, key_mask)
     return _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask)
 
 
@@ -201,20 +205,18 @@ def _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask):
 class _CrossAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, scale, kv_lens, key_mask):
-        call = _fwd_call(q, k, v, scale, kv_lens, key_mask, None)
-        o, lse = _run_fwd(call, q, k, v, kv_lens, key_mask, True)
+        o, lse = _run_fwd(_fwd_call(q, k, v, scale, kv_lens, key_mask, None), q, k, v, kv_lens, key_mask, True)
         ctx.save_for_backward(q, k, v, o, lse, kv_lens, key_mask)
-        ctx.scale, ctx.call = scale, call
+        ctx.scale = scale
         return o
 
     @staticmethod
     @first_order
     def backward(ctx, dout):
         q, k, v, o, lse, kv_lens, key_mask = ctx.saved_tensors
-        dout, calls = as_gradient(dout), ctx.call.back
-        # q, k, v and the masks are the forward's, o and lse lie as it made them: dout alone may differ
-        kind = _kind(dout)
-        call = calls.get(kind) or _keep(calls, kind, _bwd_call(q, k, v, o, lse, dout, ctx.scale, kv_lens, key_mask))
+        dout = as_gradient(dout)
+        # hooks on saved tensors may hand them back in another layout: a call is kept for what comes back
+        call = _bwd_call(q, k, v, o, lse, dout, ctx.scale, kv_lens, key_mask)
         return _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask) + (None, None, None)
 
 
