@@ -274,6 +274,9 @@ squad_status encode_rows(CUtensorMap* map, const sq::HostDevice& dev, const void
   return sq::host_encode_bf16(map, dev.device, 4, base, dims, strides, box);
 }
 
+// CTAs of a persistent launch: one an SM takes the items in turn.
+int cross_ctas(const sq::HostDevice& dev, int items) { return items < dev.sms ? items : dev.sms; }
+
 template <int D, int MASK>
 squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& maps, const sq::CrossFwdArgs& a,
                               cudaStream_t st) {
@@ -282,8 +285,7 @@ squad_status launch_cross_fwd(const sq::HostDevice& dev, const sq::CrossMaps& ma
   static std::atomic<bool> done[kMaxDevices];
   squad_status s = allow_smem(kern, Lay::BYTES, dev, done);
   if (s != SQUAD_OK) return s;
-  const int grid = a.plan.items < dev.sms ? a.plan.items : dev.sms;
-  kern<<<grid, sq::kCrossThreads, Lay::BYTES, st>>>(maps, a);
+  kern<<<cross_ctas(dev, a.plan.items), sq::kCrossThreads, Lay::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
   return SQUAD_OK;
 }
@@ -306,7 +308,8 @@ squad_status tc_cross_fwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.lse = c.lse;
   a.err = dev.err;
-  a.timeout_ns = sq::kWaitTimeoutNs;
+  a.timeout_ns = sq::cross_wait_ns(sq::kWaitTimeoutNs, a.plan.items, cross_ctas(dev, a.plan.items),
+                                   (a.plan.kblocks + a.plan.splits - 1) / a.plan.splits);
   a.part_o = c.part;
   a.part_lse = c.part_lse;
   const int mask = c.mask.keys != nullptr ? 2 : c.mask.lens != nullptr ? 1 : 0;
@@ -371,12 +374,16 @@ squad_status launch_cross_bwd(const sq::HostDevice& dev, const sq::CrossBwdMaps&
   if ((s = allow_smem(dq, sq::CrossDqLayout<D>::BYTES, dev, done_q)) != SQUAD_OK) return s;
   if ((s = allow_smem(dkv, sq::CrossDkvLayout<D>::BYTES, dev, done_kv)) != SQUAD_OK) return s;
   a.items = a.B * a.heads * a.qtiles * a.dq_splits;
-  dq<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDqLayout<D>::BYTES, st>>>(maps, a);
+  a.timeout_ns = sq::cross_wait_ns(sq::kWaitTimeoutNs, a.items, cross_ctas(dev, a.items),
+                                   (a.kblocks + a.dq_splits - 1) / a.dq_splits);
+  dq<<<cross_ctas(dev, a.items), sq::kCrossBwdThreads, sq::CrossDqLayout<D>::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
   if (a.dq_splits > 1 && (s = join_dq<__nv_bfloat16>(a.dq_part, a.dq_splits, a.B, a.heads, a.n, D, a.dq, a.sdq, st)) != SQUAD_OK)
     return s;
   a.items = a.B * a.kv_heads * a.kblocks * a.splits;
-  dkv<<<a.items < dev.sms ? a.items : dev.sms, sq::kCrossBwdThreads, sq::CrossDkvLayout<D>::BYTES, st>>>(maps, a);
+  a.timeout_ns = sq::cross_wait_ns(sq::kWaitTimeoutNs, a.items, cross_ctas(dev, a.items),
+                                   (a.group * a.qtiles + a.splits - 1) / a.splits);
+  dkv<<<cross_ctas(dev, a.items), sq::kCrossBwdThreads, sq::CrossDkvLayout<D>::BYTES, st>>>(maps, a);
   SQ_CUDA(cudaGetLastError());
   if (a.splits > 1) {
     const long long rows = (long long)a.B * a.kv_heads * a.m;
@@ -434,7 +441,6 @@ squad_status tc_cross_bwd(const sq::HostDevice& dev, const squad_cross_desc* d, 
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
   a.dq_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.dq_part);
   a.err = dev.err;
-  a.timeout_ns = sq::kWaitTimeoutNs;
   const bool masked = c.mask.lens != nullptr || c.mask.keys != nullptr;
   if (D == 128)
     return masked ? launch_cross_bwd<128, true>(dev, maps, a, st) : launch_cross_bwd<128, false>(dev, maps, a, st);

@@ -99,6 +99,15 @@ SQ_HD CrossRange cross_range(const CrossPlan& p, int len, int sp) {
   return r;
 }
 
+// The longest that a wait of the tensor-core kernels may last, in ns: `base` and 20 us for every block
+// (128 queries x 128 keys, of two jobs in the forward) that a CTA works on, `items` of `blocks` each spread
+// over `ctas`. A block takes 1 to 4 us, so the kernel as a whole takes a fifth of it at most, and
+// no wait is longer than the kernel: a role may sleep through all of it (the mask warp of a batch in
+// which only the last row's length ends inside a block), or through a job of very many keys.
+inline uint64_t cross_wait_ns(uint64_t base, long long items, long long ctas, long long blocks) {
+  return base + 20000ull * uint64_t((items + ctas - 1) / ctas) * uint64_t(blocks);
+}
+
 // How many parts the keys of a query tile are cut into (dq kernels): `tiles` query tiles over
 // `blocks` key blocks each. A part per idle SM, two blocks at least to a part. On the tensor cores
 // only for long keys, as in the forward's plan (backward of 24 heads of 128, whole / split: 1 query x

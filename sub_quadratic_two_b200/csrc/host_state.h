@@ -12,7 +12,7 @@
 
 namespace sq {
 
-constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s per wait: far above any legitimate wait
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // 2 s per wait, where no wait lasts longer than a job
 
 struct HostDevice {
   int device;
