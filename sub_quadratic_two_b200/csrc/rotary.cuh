@@ -84,6 +84,13 @@ struct Chunk<__nv_bfloat16> {
   }
 };
 
+// The first `words` words of `done`, the others of `from`: channels past the axes' keep their bits (a product with
+// cos 1 and sin 0 would turn the neighbour of an infinity into NaN).
+__device__ __forceinline__ uint4 turned_words(int words, const uint4& done, const uint4& from) {
+  return make_uint4(words > 0 ? done.x : from.x, words > 1 ? done.y : from.y, words > 2 ? done.z : from.z,
+                    words > 3 ? done.w : from.w);
+}
+
 // HALF: a thread holds the chunks at channels ca and cb of a row, element e of each being
 // one pair; else it holds one chunk with pairs inside it.
 template <typename T, bool HALF>
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int p = lane * NP + i;
-    float2 cs = make_float2(1.f, 0.f);  // channels past the axes' are copied
+    float2 cs = make_float2(1.f, 0.f);
     if (p < a.pT)
       cs = __ldg(a.table + (long long)t * a.pT + p);
     else if (p < a.pT + a.pH)
@@ -110,6 +117,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     c[i] = cs.x;
     s[i] = cs.y * a.sign;
   }
+  // words of a chunk that are turned (HALF: all or none)
+  const int words = HALF ? (lane * N < turned ? 4 : 0) : (turned - lane * NP) * (4 / NP);
   int ca = lane * N, cb = 0;
   if (HALF) {
     if (lane * N < turned) {
@@ -152,8 +161,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
         u[e] = p;
         w[e] = z;
       }
-      *reinterpret_cast<uint4*>(dst + ca * ES) = Chunk<T>::store(u);
-      *reinterpret_cast<uint4*>(dst + cb * ES) = Chunk<T>::store(w);
+      *reinterpret_cast<uint4*>(dst + ca * ES) = turned_words(words, Chunk<T>::store(u), va[i]);
+      *reinterpret_cast<uint4*>(dst + cb * ES) = turned_words(words, Chunk<T>::store(w), vb[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < NP; ++e) {
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
         u[2 * e + 1] = fmaf(u[2 * e], s[e], u[2 * e + 1] * c[e]);
         u[2 * e] = p;
       }
-      *reinterpret_cast<uint4*>(dst + ca * ES) = Chunk<T>::store(u);
+      *reinterpret_cast<uint4*>(dst + ca * ES) = turned_words(words, Chunk<T>::store(u), va[i]);
     }
   }
 }

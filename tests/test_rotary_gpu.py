@@ -234,3 +234,24 @@ def test_refusals(cuda_ok):
         sq.squad_rotary([x[..., 1:33]], sq.rotary_plan((1, 2, 3), 32))  # 4 bytes off
     with pytest.raises(sq.SquadError):
         sq.squad_rotary([x[..., :32]], sq.rotary_plan((1, 2, 3), 64))  # a table of more channels than d
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,axes,pairing", [
+    (128, (20, 6, 6), "adjacent"), (64, (2, 0, 0), "adjacent"), (64, (0, 0, 0), "adjacent"), (64, (0, 0, 0), "half"),
+    (128, (32, 16, 16), "half"), (96, (2, 4, 8), "adjacent")])
+def test_copied_channels_are_copied(cuda_ok, dtype, d, axes, pairing):
+    # channels past the axes', whatever their neighbours hold: infinities, NaN and signed zeros bit by bit
+    grid, n = (2, 3, 5), 30
+    rot = sq.rotary_plan(grid, d, axes, pairing=pairing, offset=(3, 0, 1))
+    r = sum(axes)
+    x = torch.randn(2, 3, n, d, generator=torch.Generator(device="cuda").manual_seed(d + r), device="cuda").to(dtype)
+    finite = x.clone()
+    odd = torch.tensor([float("inf"), -0.0, float("nan"), 0.0, -float("inf"), -1.0, 0.0], device="cuda").to(dtype)
+    x[..., r:] = odd[torch.arange(d - r, device="cuda") % 7]
+    for inverse in (False, True):
+        (y,) = sq.squad_rotary([x], rot, inverse=inverse)
+        bits = torch.int16 if dtype == BF16 else torch.int32
+        assert torch.equal(y[..., r:].contiguous().view(bits), x[..., r:].contiguous().view(bits))
+        # and they leave the turned channels alone
+        assert torch.equal(y[..., :r], sq.squad_rotary([finite], rot, inverse=inverse)[0][..., :r])
