@@ -379,10 +379,15 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x, ++job) {
       if (!(ok = make_d_if(i + int(gridDim.x)))) break;
       const Item it = item_of(i);
+      const int tok = it.qt * 128 + row;
+      // a query without keys gets zeros, whatever its dO holds (0 times an infinite dP - D is NaN)
+      const float sc = MASKED && tok < args.n &&
+                               __ldg(args.lse + ((long long)it.b * args.heads + it.h) * args.n + tok) == -INFINITY
+                           ? 0.f
+                           : args.scale;
       if (!(ok = cross_warp_wait(&bars[Lay::OF], job & 1, abort_flag, to))) break;
       tc_fence_after();
       const uint32_t t = tmem + (uint32_t(ew * 32) << 16) + 384;
-      const int tok = it.qt * 128 + row;
       __nv_bfloat16* out = args.dq + it.b * args.sdq.b + it.h * args.sdq.h + (long long)tok * args.sdq.n;
       float* part = args.dq_part +
                     (((long long)it.sp * args.B * args.heads + (long long)it.b * args.heads + it.h) * args.n + tok) * D;
@@ -391,13 +396,14 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
         uint32_t v[32];
         __syncwarp();  // lanes part below: TMEM is read by whole warps
         tmem_ld32(t + c, v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          v[e] = MASKED && sc == 0.f ? 0u : __float_as_uint(__uint_as_float(v[e]) * sc);
         if (args.dq_splits > 1) {
           if (tok < args.n) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(part + c + e) = make_float4(
-                  __uint_as_float(v[e]) * args.scale, __uint_as_float(v[e + 1]) * args.scale,
-                  __uint_as_float(v[e + 2]) * args.scale, __uint_as_float(v[e + 3]) * args.scale);
+              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         } else if (tok < args.n) {
 #pragma unroll
@@ -405,8 +411,7 @@ __global__ void __launch_bounds__(kCrossBwdThreads, 1)
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              p[e] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * args.scale,
-                                 __uint_as_float(v[8 * j + 2 * e + 1]) * args.scale);
+              p[e] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
             *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(p[0], p[1], p[2], p[3]);
           }
         }

@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = th.x + 16 * j;
-        const float p = keep[c] != 0.f ? expf(s[i][j] * a.scale - lse[r]) : 0.f;
-        ps[r * Lay::PW + Lay::place(c)] = p * (dp[i][j] - dd[r]);
+        // 0 for a key that does not count, whatever dO holds
+        ps[r * Lay::PW + Lay::place(c)] = keep[c] != 0.f ? expf(s[i][j] * a.scale - lse[r]) * (dp[i][j] - dd[r]) : 0.f;
       }
     }
     __syncthreads();
@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kF32Threads, kF32DkdvBlocks<D>) cross_f32_dkdv
   for (int i = 0; i < R; ++i) {
     const int j = j0 + th.result_row(i);
     if (j >= a.m) continue;
+    const bool live = keep[th.result_row(i)] != 0.f;  // else zeros, whatever q and dO hold
     const long long row = ((long long)b * a.kv_heads + hk) * a.m + j;
     float* ok = a.splits > 1 ? a.part + (sp * rows + row) * D : cross_row<float>(a.dk, a.sdk, b, hk, j);
     float* ov = a.splits > 1 ? a.part + ((a.splits + sp) * rows + row) * D : cross_row<float>(a.dv, a.sdv, b, hk, j);
@@ -458,8 +459,11 @@ __global__ void __launch_bounds__(kF32Threads, kF32DkdvBlocks<D>) cross_f32_dkdv
       if (D % 64 != 0 && th.c + 16 * k >= D / 4) continue;
       const int c = 4 * (th.c + 16 * k);
       const float *vk = dk + 4 * (Lay::NC * i + k), *vv = dv + 4 * (Lay::NC * i + k);
-      *reinterpret_cast<float4*>(ok + c) = make_float4(vk[0] * a.scale, vk[1] * a.scale, vk[2] * a.scale, vk[3] * a.scale);
-      *reinterpret_cast<float4*>(ov + c) = make_float4(vv[0], vv[1], vv[2], vv[3]);
+      float4 gk = make_float4(vk[0] * a.scale, vk[1] * a.scale, vk[2] * a.scale, vk[3] * a.scale);
+      float4 gv = make_float4(vv[0], vv[1], vv[2], vv[3]);
+      if (!live) gk = gv = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(ok + c) = gk;
+      *reinterpret_cast<float4*>(ov + c) = gv;
     }
   }
 }

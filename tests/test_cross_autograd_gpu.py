@@ -35,3 +35,41 @@ def test_saved_tensors_kept_on_the_host(cuda_ok, dtype, offloaded_first):
         for name, g, r, b in zip(("dq", "dk", "dv"), grads, want, bs[2:]):
             assert_within(g, r, b, name)
     sq.poll_device_error()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,m", [(5, 9), (300, 200), (130, 700), (1, 3000)])
+def test_queries_without_states_give_no_gradient_whatever_comes_in(cuda_ok, dtype, n, m):
+    # dout of a query without states may be infinite or NaN (a loss over padded rows, say), and so may the query
+    B, d = 4, 64
+    q, k, v, do = problem(61, B, 4, 2, n, m, d, dtype)
+    q[1], do[1], do[2], do[3] = float("nan"), float("inf"), float("nan"), -float("inf")
+    mask = torch.ones(B, m, dtype=torch.bool, device="cuda")
+    mask[1:] = False
+    lens = torch.tensor([m, 0, 0, 0], dtype=torch.int32, device="cuda")
+    keep, s = keep_of(1, m), d ** -0.5
+    bs, want = bounds(q[:1], k[:1], v[:1], keep, s, do[:1])[2:], backward(q[:1], k[:1], v[:1], keep, s, do[:1])
+    for kw in (dict(key_mask=mask), dict(kv_lens=lens), dict(key_mask=mask, kv_lens=lens)):
+        o, lse = sq.squad_cross_fwd(q, k, v, **kw)
+        for name, g, r, b in zip(("dq", "dk", "dv"), sq.squad_cross_bwd(q, k, v, o, lse, do, **kw), want, bs):
+            assert (g[1:] == 0).all(), name
+            assert_within(g[:1], r, b, name)
+    sq.poll_device_error()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,m", [(5, 9), (300, 200), (700, 130), (1, 3000)])
+def test_states_that_do_not_count_get_zeros_whatever_comes_in(cuda_ok, dtype, n, m):
+    B, d = 2, 64
+    q, k, v, do = problem(63, B, 4, 2, n, m, d, dtype)
+    do[0, 1, n // 2], q[1, 3, 0] = float("nan"), float("inf")
+    mask = torch.rand(B, m, generator=torch.Generator().manual_seed(m)).cuda() < 0.6
+    mask[:, 0] = True
+    lens = torch.tensor([m - 1, 1], dtype=torch.int32, device="cuda")
+    for kw in (dict(key_mask=mask), dict(kv_lens=lens), dict(key_mask=mask, kv_lens=lens)):
+        dead = ~keep_of(B, m, kw.get("kv_lens"), kw.get("key_mask"))
+        o, lse = sq.squad_cross_fwd(q, k, v, **kw)
+        _, dk, dv = sq.squad_cross_bwd(q, k, v, o, lse, do, **kw)
+        for g in (dk, dv):
+            assert (g.transpose(1, 2)[dead] == 0).all()
+    sq.poll_device_error()
