@@ -12,6 +12,7 @@ from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _check, _dtype_code, load_library
@@ -40,10 +41,26 @@ def raw_stream(dev: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def in_dual_level() -> bool:
+    """Whether forward-mode differentiation is on: tensors may carry tangents then, without requires_grad, and only
+    an autograd function (which has no formula for them, and says so) sees them."""
+    return forward_ad._current_level >= 0
+
+
+def has_tangent(*ts) -> bool:
+    return in_dual_level() and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in ts)
+
+
 def first_order(backward):
-    """once_differentiable (a second differentiation raises), without its 3 us where none can follow."""
+    """once_differentiable (a second differentiation raises), without its 3 us where none can follow; a tangent of
+    the incoming gradients raises too."""
     once = once_differentiable(backward)
-    return lambda ctx, *grads: once(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    def run(ctx, *grads):
+        if has_tangent(*grads):
+            raise RuntimeError("gradients are not differentiable again: forward-mode tangents have no formula here")
+        return once(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return run
 
 
 def token_major(t: torch.Tensor) -> bool:
@@ -254,9 +271,10 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary):
     """(q, k) turned by the grid's positions, as contiguous [B, heads, T*H*W, d] tensors (float32 or bfloat16).
 
     k may have its own number of heads, or be None (then None comes back in its place). Differentiable; the
-    gradients come in the memory layout of q and k.
+    gradients come in the memory layout of q and k. Forward-mode tangents are refused (RuntimeError).
     """
     xs = (q,) if k is None else (q, k)
-    # without a gradient to come there is nothing for autograd to record
-    ys = _Rotary.apply(rot, *xs) if torch.is_grad_enabled() and any(x.requires_grad for x in xs) else squad_rotary(xs, rot)
+    # without a derivative to come there is nothing for autograd to record
+    record = in_dual_level() or torch.is_grad_enabled() and any(x.requires_grad for x in xs)
+    ys = _Rotary.apply(rot, *xs) if record else squad_rotary(xs, rot)
     return ys[0], None if k is None else ys[1]

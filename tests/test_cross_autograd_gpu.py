@@ -73,3 +73,25 @@ def test_states_that_do_not_count_get_zeros_whatever_comes_in(cuda_ok, dtype, n,
         for g in (dk, dv):
             assert (g.transpose(1, 2)[dead] == 0).all()
     sq.poll_device_error()
+
+
+def test_forward_mode_is_refused(cuda_ok):
+    # a tangent has no formula here: it must not be lost
+    grid = (1, 2, 3)
+    rot = sq.rotary_plan(grid, 64)
+    x, t = torch.randn(1, 2, 6, 64, device="cuda"), torch.randn(1, 2, 6, 64, device="cuda")
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        dual = fw.make_dual(x, t)
+        for call in (lambda: sq.cross_attention(dual, x, x), lambda: sq.cross_attention(x, dual, x),
+                     lambda: sq.cross_attention(x, x, dual), lambda: sq.rotary(dual, None, rot),
+                     lambda: sq.rotary(x, dual, rot), lambda: sq.attention(dual, x, x, grid, (1, 1, 3), rotary=rot),
+                     lambda: sq.attention(x, x, dual, grid, (1, 1, 3), rotary=rot)):
+            with pytest.raises(RuntimeError):
+                call()
+            with torch.no_grad(), pytest.raises(RuntimeError):
+                call()
+        # without tangents a call is as it is outside
+        assert torch.equal(sq.cross_attention(x, x, x), sq.squad_cross_fwd(x, x, x)[0])
+        y, z = sq.rotary(x, None, rot)
+        assert z is None and torch.equal(y, sq.squad_rotary([x], rot)[0])

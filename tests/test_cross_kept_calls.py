@@ -67,3 +67,27 @@ def test_saved_tensors_of_another_kind_are_not_run_with_a_kept_call(launches):
         o = sq.cross_attention(q, k, v)
     torch.autograd.grad(o, q, torch.ones_like(o))
     assert [desc.m for desc, _ in launches] == [9, 5]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_forward_mode_tangents_are_refused(launches, which):
+    ts = [torch.randn(1, 2, 6, 64) for _ in range(3)]
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        sq.cross_attention(*ts)
+        ts[which] = fw.make_dual(ts[which], torch.ones_like(ts[which]))
+        with pytest.raises(RuntimeError, match="jvp"):
+            sq.cross_attention(*ts)
+        with torch.no_grad(), pytest.raises(RuntimeError, match="jvp"):
+            sq.cross_attention(*ts)
+
+
+def test_a_tangent_of_the_incoming_gradient_is_refused(launches):
+    q, k, v = (torch.randn(1, 2, 6, 64, requires_grad=True) for _ in range(3))
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        o = sq.cross_attention(q, k, v)
+        dout = torch.ones_like(o)
+        torch.autograd.grad(o, q, dout, retain_graph=True)
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            torch.autograd.grad(o, q, fw.make_dual(dout, dout))
