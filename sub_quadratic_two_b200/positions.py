@@ -115,6 +115,7 @@ class Rotary:
     axes: channels turned by time, height and width (even, their sum at most d; channels past it are copied).
     table: [T*axes[0]/2 + H*axes[1]/2 + W*axes[2]/2, 2] float32 CUDA tensor of (cos, sin): per axis one row
     of pairs for each position. pairing: "adjacent" turns channels (2i, 2i+1), "half" (i, i + sum(axes)/2).
+    The table is a constant: `rotary` refuses one that wants a gradient.
     """
     grid: Tuple[int, int, int]
     axes: Tuple[int, int, int]
@@ -271,9 +272,12 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary):
     """(q, k) turned by the grid's positions, as contiguous [B, heads, T*H*W, d] tensors (float32 or bfloat16).
 
     k may have its own number of heads, or be None (then None comes back in its place). Differentiable; the
-    gradients come in the memory layout of q and k. Forward-mode tangents are refused (RuntimeError).
+    gradients come in the memory layout of q and k. Forward-mode tangents are refused (RuntimeError), and so is
+    a table that requires a gradient or carries a tangent (ValueError; under no_grad a table may require one).
     """
     xs = (q,) if k is None else (q, k)
+    if torch.is_grad_enabled() and rot.table.requires_grad or has_tangent(rot.table):
+        raise ValueError("the rotary table is a constant: it has no gradient (pass table.detach())")
     # without a derivative to come there is nothing for autograd to record
     record = in_dual_level() or torch.is_grad_enabled() and any(x.requires_grad for x in xs)
     ys = _Rotary.apply(rot, *xs) if record else squad_rotary(xs, rot)

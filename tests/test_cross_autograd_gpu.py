@@ -95,3 +95,24 @@ def test_forward_mode_is_refused(cuda_ok):
         assert torch.equal(sq.cross_attention(x, x, x), sq.squad_cross_fwd(x, x, x)[0])
         y, z = sq.rotary(x, None, rot)
         assert z is None and torch.equal(y, sq.squad_rotary([x], rot)[0])
+
+
+def test_a_table_that_wants_a_gradient_is_refused(cuda_ok):
+    rot = sq.rotary_plan((1, 2, 3), 64)
+    x = torch.randn(1, 2, 6, 64, device="cuda")
+    learned = sq.Rotary(rot.grid, rot.axes, rot.table.clone().requires_grad_())
+    for q in (x, x.clone().requires_grad_()):
+        for call in (lambda: sq.rotary(q, None, learned), lambda: sq.rotary(q, q, learned),
+                     lambda: sq.attention(q, q, q, (1, 2, 3), (1, 1, 3), rotary=learned),
+                     lambda: sq.attention_multi(q, q, q, (1, 2, 3), [(1, 1, 3)], rotary=learned)):
+            with pytest.raises(ValueError):
+                call()
+    with torch.no_grad():
+        assert torch.equal(sq.rotary(x, None, learned)[0], sq.rotary(x, None, rot)[0])
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        dual = sq.Rotary(rot.grid, rot.axes, fw.make_dual(rot.table, torch.ones_like(rot.table)))
+        with pytest.raises(ValueError):
+            sq.rotary(x, None, dual)
+        with torch.no_grad(), pytest.raises(ValueError):
+            sq.rotary(x, None, dual)

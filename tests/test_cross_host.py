@@ -150,3 +150,13 @@ def test_rotary_plan_refusals():
         sq.squad_rotary([torch.zeros(1, 1, 24, 64)], sq.Rotary((2, 3, 4), (24, 20, 20), t))  # host tensors
     with pytest.raises(ValueError):
         sq.cross_attention(*[torch.zeros(1, 1, 4, 64)] * 3)
+
+
+def test_a_rotary_table_is_a_constant():
+    t = torch.zeros(2 * 12 + 3 * 10 + 4 * 10, 2, requires_grad=True)
+    x = torch.zeros(1, 1, 24, 64)
+    with pytest.raises(ValueError, match="constant"):
+        sq.rotary(x, None, sq.Rotary((2, 3, 4), (24, 20, 20), t))
+    fw = torch.autograd.forward_ad
+    with fw.dual_level(), pytest.raises(ValueError, match="constant"):
+        sq.rotary(x, None, sq.Rotary((2, 3, 4), (24, 20, 20), fw.make_dual(t.detach(), torch.ones(t.shape))))
