@@ -8,8 +8,8 @@ from typing import Optional
 import torch
 
 from . import _check, _check_aux, _dtype_code, load_library
-from .positions import (SquadStrides, as_gradient, check_strided, empty_like_layout, first_order, in_dual_level,
-                        on_device, raw_stream)
+from .positions import (SquadStrides, as_gradient, check_strided, empty_like_layout, first_order, has_tangent,
+                        in_dual_level, on_device, raw_stream)
 
 
 class SquadCrossDesc(ctypes.Structure):
@@ -227,13 +227,16 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Op
 
     float32 or bfloat16 CUDA tensors, n and m free of each other, heads a multiple of kv_heads. Rows may be
     strided (token-major [B, n, heads, d] memory seen through transpose(1, 2)); the output lies as q does.
-    kv_lens: [B] int32, the states of each batch row that count; key_mask: [B, m] (or [1, m]) bool, True
-    where a state counts. A query with no state left gets zeros and gives no gradient. Gradients are not
-    differentiable again, and forward-mode tangents are refused (RuntimeError). A step captured into a CUDA
-    graph takes its gradients for leaves of its own (``t.detach().requires_grad_()`` shares t's memory): a leaf
-    that an eager graph still holds ties torch's autograd to the stream of that graph, outside the capture, and
-    the capture fails.
+    scale: a positive constant, None (or 0, as in `attention`) for 1/sqrt(d); a tensor is read on the host and
+    must not want a gradient (ValueError). kv_lens: [B] int32, the states of each batch row that count;
+    key_mask: [B, m] (or [1, m]) bool, True where a state counts. A query with no state left gets zeros and gives
+    no gradient. Gradients are not differentiable again, and forward-mode tangents are refused (RuntimeError). A
+    step captured into a CUDA graph takes its gradients for leaves of its own (``t.detach().requires_grad_()``
+    shares t's memory): a leaf that an eager graph still holds ties torch's autograd to the stream of that graph,
+    outside the capture, and the capture fails.
     """
+    if isinstance(scale, torch.Tensor) and (torch.is_grad_enabled() and scale.requires_grad or has_tangent(scale)):
+        raise ValueError("scale is a constant: it has no gradient (pass float(scale))")
     if in_dual_level() or torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _CrossAttention.apply(q, k, v, _scale(scale), kv_lens, key_mask)
     return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save=False)[0]

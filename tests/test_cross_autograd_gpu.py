@@ -116,3 +116,13 @@ def test_a_table_that_wants_a_gradient_is_refused(cuda_ok):
             sq.rotary(x, None, dual)
         with torch.no_grad(), pytest.raises(ValueError):
             sq.rotary(x, None, dual)
+
+
+def test_a_scale_that_wants_a_gradient_is_refused(cuda_ok):
+    q, k, v, _ = problem(62, 1, 2, 2, 6, 9, 64)
+    scale = torch.tensor(0.1, requires_grad=True)
+    for t in (q, q.clone().requires_grad_()):
+        with pytest.raises(ValueError):
+            sq.cross_attention(t, k, v, scale=scale)
+    with torch.no_grad():
+        assert torch.equal(sq.cross_attention(q, k, v, scale=scale), sq.cross_attention(q, k, v, scale=scale.item()))

@@ -91,3 +91,15 @@ def test_a_tangent_of_the_incoming_gradient_is_refused(launches):
         torch.autograd.grad(o, q, dout, retain_graph=True)
         with pytest.raises(RuntimeError, match="forward-mode"):
             torch.autograd.grad(o, q, fw.make_dual(dout, dout))
+
+
+def test_a_scale_that_wants_a_gradient_is_refused(launches):
+    q, k, v = (torch.randn(1, 2, 6, 64) for _ in range(3))
+    scale = torch.tensor(0.1, requires_grad=True)
+    for t in (q, q.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="constant"):
+            sq.cross_attention(t, k, v, scale=scale)
+    sq.cross_attention(q, k, v, scale=scale.detach())
+    fw = torch.autograd.forward_ad
+    with fw.dual_level(), pytest.raises(ValueError, match="constant"):
+        sq.cross_attention(q, k, v, scale=fw.make_dual(scale.detach(), torch.tensor(1.0)))
