@@ -9,7 +9,7 @@ import torch
 
 from . import _check, _check_aux, _dtype_code, load_library
 from .positions import (SquadStrides, as_gradient, check_strided, empty_like_layout, first_order, has_tangent,
-                        in_dual_level, on_device, raw_stream)
+                        in_dual_level, on_device, on_stream, raw_stream)
 
 
 class SquadCrossDesc(ctypes.Structure):
@@ -156,7 +156,7 @@ def squad_cross_fwd(q, k, v, scale: Optional[float] = None, kv_lens: Optional[to
     o lies in memory as q does (token-major or head-major), or in ``out``, which must not overlap an input.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with on_stream(stream, q):
             return squad_cross_fwd(q, k, v, scale, kv_lens, key_mask, save, out)
     scale = _scale(scale)
     return _run_fwd(_fwd_call(q, k, v, scale, kv_lens, key_mask, out), q, k, v, kv_lens, key_mask, save, out)
@@ -183,7 +183,7 @@ def squad_cross_bwd(q, k, v, o, lse, dout, scale: Optional[float] = None, kv_len
                     key_mask: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """Backward through the C ABI. Returns (dq, dk, dv), each lying in memory as q, k and v do."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with on_stream(stream, q):
             return squad_cross_bwd(q, k, v, o, lse, dout, scale, kv_lens, key_mask)
     call = _bwd_call(q, k, v, o, lse, dout, _scale(scale), kv_lens, key_mask)
     return _run_bwd(call, q, k, v, o, lse, dout, kv_lens, key_mask)

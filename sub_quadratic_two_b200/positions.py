@@ -41,6 +41,13 @@ def raw_stream(dev: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def on_stream(stream: torch.cuda.Stream, t):
+    """A context in which stream is current, for a call on t: the call allocates and launches on it."""
+    if isinstance(t, torch.Tensor) and stream.device != t.device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def in_dual_level() -> bool:
     """Whether forward-mode differentiation is on: tensors may carry tangents then, without requires_grad, and only
     an autograd function (which has no formula for them, and says so) sees them."""
@@ -210,11 +217,11 @@ def squad_rotary(xs: Sequence[torch.Tensor], rot: Rotary, inverse: bool = False,
     inverse turns by the opposite angles. out: tensors to write (any strides of whole 16-byte steps; an input
     itself for the rotation in place), else contiguous ones are made.
     """
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return squad_rotary(xs, rot, inverse, out)
     if not xs:
         raise ValueError("one or two tensors")
+    if stream is not None:
+        with on_stream(stream, xs[0]):
+            return squad_rotary(xs, rot, inverse, out)
     # (empty_like is the shortest way to a contiguous tensor: 1.3 us where new_empty takes 2.4)
     ys = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs] if out is None else list(out)
     ref, last = xs[0], xs[-1]

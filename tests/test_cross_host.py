@@ -160,3 +160,16 @@ def test_a_rotary_table_is_a_constant():
     fw = torch.autograd.forward_ad
     with fw.dual_level(), pytest.raises(ValueError, match="constant"):
         sq.rotary(x, None, sq.Rotary((2, 3, 4), (24, 20, 20), fw.make_dual(t.detach(), torch.ones(t.shape))))
+
+
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    other = SimpleNamespace(device=torch.device("cuda", 1))
+    x = torch.zeros(1, 1, 24, 64)
+    with pytest.raises(ValueError, match="stream"):
+        sq.squad_cross_fwd(x, x, x, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        sq.squad_cross_bwd(x, x, x, x, x[..., 0], x, stream=other)
+    t = torch.zeros(2 * 12 + 3 * 10 + 4 * 10, 2)
+    with pytest.raises(ValueError, match="stream"):
+        sq.squad_rotary([x], sq.Rotary((2, 3, 4), (24, 20, 20), t), stream=other)
