@@ -211,6 +211,8 @@ squad_status f32_cross_dq(const sq::HostDevice& dev, const sq::CrossArgs& a, cud
 template <int D, int R>
 squad_status f32_cross_dkdv(const sq::HostDevice& dev, const sq::CrossArgs& a, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
+  // the blocks that the plan counts on (228 KB an SM, 1 of them reserved for each)
+  static_assert(sq::cross_f32_dkdv_blocks(D) * (sq::F32Layout<D, R>::DKV + 1024) <= 228 * 1024, "blocks of an SM");
   auto dkv = sq::cross_f32_dkdv_kernel<D, R>;
   squad_status s;
   if ((s = allow_smem(dkv, sq::F32Layout<D, R>::DKV, dev, done)) != SQUAD_OK) return s;
@@ -241,7 +243,7 @@ template <F32Kernel WHICH>
 squad_status f32_cross(const sq::HostDevice& dev, int r, const sq::CrossArgs& a, cudaStream_t st) {
 #define SQ_D(N)                                                                                         \
   case N:                                                                                               \
-    return r == 4   ? f32_cross_run<WHICH, N, (WHICH == kF32Dkdv && N <= 160 ? 4 : 2)>(dev, a, st)      \
+    return r == 4   ? f32_cross_run<WHICH, N, (WHICH == kF32Dkdv ? sq::cross_f32_dkdv_rows(N) : 2)>(dev, a, st) \
            : r == 2 ? f32_cross_run<WHICH, N, 2>(dev, a, st)                                            \
                     : f32_cross_run<WHICH, N, 1>(dev, a, st)
   switch (a.d) {

@@ -16,6 +16,7 @@
 #pragma once
 #include <cstdint>
 #include "cross_args.h"
+#include "cross_plan.h"
 #include "geometry.h"
 
 namespace sq {
@@ -381,16 +382,11 @@ __global__ void __launch_bounds__(kF32Threads) cross_f32_dq_kernel(const __grid_
   }
 }
 
-// Blocks of the dk, dv kernel that share an SM (a tile's loads under the other's products): at
-// d = 96 the 128 registers that leaves cost nothing and 24 heads, 300 x 300 take 99 in place of 131
-// us; at d = 128 they spill.
-template <int D>
-constexpr int kF32DkdvBlocks = D <= 96 ? 2 : 1;
-
 // A block: 16 R keys and one part of the queries of their head group (blockIdx.x = key tile *
 // splits + part); with splits > 1 the parts go to a.part, [dk, dv][split][B, kv_heads, m][D].
 template <int D, int R>
-__global__ void __launch_bounds__(kF32Threads, kF32DkdvBlocks<D>) cross_f32_dkdv_kernel(const __grid_constant__ CrossArgs a) {
+__global__ void __launch_bounds__(kF32Threads, cross_f32_dkdv_blocks(D))
+    cross_f32_dkdv_kernel(const __grid_constant__ CrossArgs a) {
   using Lay = F32Layout<D, R>;
   constexpr int LD = Lay::LD;
   extern __shared__ __align__(16) float f32_smem[];

@@ -143,10 +143,19 @@ inline int cross_dkv_splits(long long units, int tiles) {
   return best;
 }
 
+// Blocks of the fp32 dk, dv kernel that share an SM, a tile's loads under the other's products: two where the 128
+// registers a thread that it leaves cost nothing (24 heads of 96, 300 x 300: 99 in place of 131 us); at d = 128
+// they spill.
+constexpr int cross_f32_dkdv_blocks(int d) { return d <= 96 ? 2 : 1; }
+// The most keys of a block, in 16s: 64, or 32 where the registers (d > 160) or two blocks' shared memory (d = 96:
+// 135 KB for 64 keys) do not hold more. One block of 64 keys in place of two of 32, d = 96: 8 heads, 4,096 x 1,024
+// backward 1,956 for 1,760 us, 2,000 x 500 517 for 472.
+constexpr int cross_f32_dkdv_rows(int d) { return d <= 64 || (d > 96 && d <= 160) ? 4 : 2; }
+
 // The dk, dv kernel in fp32: 16 `rows` keys to a block, and parts of the queries of a key tile.
 // The least of, in us (fitted to 12 sizes of 77 to 4,096 rows, to within a quarter): for each
 // round of the blocks over the SMs, per 64 queries (1.1 + 2.2 rows) d / 64, and two thirds of that to
-// begin and end; where two blocks share an SM (d <= 96) together one and a half times as long;
+// begin and end; where two blocks share an SM together one and a half times as long;
 // 2.5 and the parts' traffic where there is something to join. 16 rows and the parts of
 // the rule above in its place: 17.1 for 8.3 us at 2 heads of 64, 256 x 77; 76 for 45 at 8 of 32,
 // 1,500 x 200; 1,478 for 971 at 8 of 128, 4,096 x 1,024.
@@ -155,15 +164,16 @@ struct CrossF32Dkdv {
 };
 inline CrossF32Dkdv cross_f32_dkdv_plan(long long kv_heads, int group, int n, int m, int d) {
   const long long tiles = (long long)group * ((n + 63) / 64);
+  const long long share = cross_f32_dkdv_blocks(d), per = share * kCrossPlanSms;
   CrossF32Dkdv best{1, 1};
   double best_cost = 0;
-  for (int r = 1; r <= (d <= 160 ? 4 : 2); r *= 2) {
+  for (int r = 1; r <= cross_f32_dkdv_rows(d); r *= 2) {
     const long long units = kv_heads * ((m + 16 * r - 1) / (16 * r));
     const double step = (1.1 + 2.2 * r) * d / 64;
     for (int s = 1; s <= 64 && s <= tiles; ++s) {
-      const long long blocks = units * s, per = d <= 96 ? 2 * kCrossPlanSms : kCrossPlanSms;
+      const long long blocks = units * s;
       if (s > 1 && blocks > 4 * per) break;  // more parts only add to the join
-      const double rounds = double((blocks + per - 1) / per) * (d <= 96 && blocks > kCrossPlanSms ? 1.5 : 1.0);
+      const double rounds = double((blocks + per - 1) / per) * (share > 1 && blocks > kCrossPlanSms ? 1.5 : 1.0);
       const double cost = rounds * step * (double((tiles + s - 1) / s) + 0.67) +
                           (s > 1 ? 2.5 + 16.0 * s * double(kv_heads) * m * d / 4e6 : 0.0);
       if (best_cost == 0 || cost < best_cost) {
