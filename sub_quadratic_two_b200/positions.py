@@ -115,9 +115,9 @@ def default_axes(d: int) -> Tuple[int, int, int]:
     return d - 2 * side, side, side
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class Rotary:
-    """The rotation of a T x H x W grid.
+    """The rotation of a T x H x W grid. Two plans are equal where they are one (tables are not compared).
 
     axes: channels turned by time, height and width (even, their sum at most d; channels past it are copied).
     table: [T*axes[0]/2 + H*axes[1]/2 + W*axes[2]/2, 2] float32 CUDA tensor of (cos, sin): per axis one row

@@ -173,3 +173,8 @@ def test_a_stream_of_another_device_is_refused():
     t = torch.zeros(2 * 12 + 3 * 10 + 4 * 10, 2)
     with pytest.raises(ValueError, match="stream"):
         sq.squad_rotary([x], sq.Rotary((2, 3, 4), (24, 20, 20), t), stream=other)
+
+
+def test_rotary_plans_compare_and_are_kept_in_sets():
+    a, b = (sq.rotary_plan((1, 2, 3), 64, device="cpu") for _ in range(2))
+    assert a == a and a != b and b in [a, b] and {a: 1, b: 2}[b] == 2
