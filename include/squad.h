@@ -312,7 +312,8 @@ typedef struct {
 /* One launch over 1 or 2 tensors (queries and keys): y[i] = rotation of x[i], of
  * heads[i] heads, with strides xs[i] and ys[i]. Every pointer and every stride (of
  * an extent above 1) is a multiple of 16 bytes; y[i] may be x[i] with equal
- * strides, else the tensors must not overlap. Products and sums in fp32, one
+ * strides, else the tensors must not overlap (SQUAD_ERR_INVALID_ARG where an output begins
+ * at another tensor's first element). Products and sums in fp32, one
  * rounding to the output. Limits (SQUAD_ERR_UNSUPPORTED): d a multiple of 16
  * bytes, d <= 1024; SQUAD_ROTARY_HALF: r and d - r multiples of 32 bytes. */
 squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int* heads, const void* const* x,
@@ -335,7 +336,8 @@ squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int
  * [B, n, heads, d] memory is as good as head-major. Pointers and strides (of
  * extents above 1) are multiples of 16 bytes; batch and head strides of inputs may
  * be 0 (broadcast). scale <= 0 selects 1/sqrt(d). lse [B, heads, n] fp32, contiguous.
- * No two rows of an output overlap (SQUAD_ERR_ALIGN), nor an output and another or an input.
+ * No two rows of an output overlap (SQUAD_ERR_ALIGN), nor an output and another or an input
+ * (SQUAD_ERR_INVALID_ARG where they begin at the same element).
  * Limits (SQUAD_ERR_UNSUPPORTED): bf16 d in {64, 128}; f32 d a multiple of 32,
  * d <= 256; B and heads <= 65535. */
 typedef struct {

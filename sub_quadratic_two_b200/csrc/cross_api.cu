@@ -59,6 +59,10 @@ bool stride_ok(const squad_strides& s, int B, int h, int n, int d, size_t elem, 
   return true;
 }
 
+bool same_rows(const squad_strides& a, const squad_strides& b, int B, int h, int n) {
+  return (B <= 1 || a.b == b.b) && (h <= 1 || a.h == b.h) && (n <= 1 || a.n == b.n);
+}
+
 // ---------------------------------------------------------------- cross attention
 
 squad_status check_cross(const squad_cross_desc* d) {
@@ -480,6 +484,7 @@ squad_status squad_cross_fwd(const squad_cross_desc* desc, const void* q, const 
   if (reinterpret_cast<uintptr_t>(kv_lens) & 3u) return SQUAD_ERR_ALIGN;
   if ((s = check_cross_strides(desc, false)) != SQUAD_OK) return s;
   if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return SQUAD_ERR_WORKSPACE;
+  if (o == q || o == k || o == v) return SQUAD_ERR_INVALID_ARG;
   sq::HostDevice dev;
   if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
   sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
@@ -508,6 +513,10 @@ squad_status squad_cross_bwd(const squad_cross_desc* desc, const void* q, const 
   if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u)) return SQUAD_ERR_ALIGN;
   if ((s = check_cross_strides(desc, true)) != SQUAD_OK) return s;
   if (workspace == nullptr || workspace_bytes < w.total) return SQUAD_ERR_WORKSPACE;
+  for (const void* out : {dq, dk, dv})
+    for (const void* in : {q, k, v, o, dout})
+      if (out == in) return SQUAD_ERR_INVALID_ARG;
+  if (dq == dk || dq == dv || dk == dv) return SQUAD_ERR_INVALID_ARG;
   sq::HostDevice dev;
   if ((s = sq::host_device(&dev)) != SQUAD_OK) return s;
   sq::CrossArgs a = cross_args(desc, q, k, v, kv_lens, key_mask);
@@ -567,6 +576,12 @@ squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int
               xs[i].n * es, ys[i].b * es, ys[i].h * es, ys[i].n * es, heads[i]};
   }
   if (reinterpret_cast<uintptr_t>(table) & 7u) return SQUAD_ERR_ALIGN;
+  // an output may be its own input, row for row, and no other tensor
+  for (int i = 0; i < ntensors; ++i)
+    for (int j = 0; j < ntensors; ++j) {
+      if (i != j && (y[i] == y[j] || y[i] == x[j])) return SQUAD_ERR_INVALID_ARG;
+      if (i == j && y[i] == x[i] && !same_rows(xs[i], ys[i], d.B, heads[i], int(n))) return SQUAD_ERR_INVALID_ARG;
+    }
   const long long groups = (total + sq::kRotaryHeads - 1) / sq::kRotaryHeads;
   if (groups > kMaxGridYZ) return SQUAD_ERR_UNSUPPORTED;
   a.table = reinterpret_cast<const float2*>(table);

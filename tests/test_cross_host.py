@@ -178,3 +178,28 @@ def test_a_stream_of_another_device_is_refused():
 def test_rotary_plans_compare_and_are_kept_in_sets():
     a, b = (sq.rotary_plan((1, 2, 3), 64, device="cpu") for _ in range(2))
     assert a == a and a != b and b in [a, b] and {a: 1, b: 2}[b] == 2
+
+
+def test_outputs_that_begin_at_another_tensor_are_refused(lib):
+    # every call here has such an output: nothing is launched
+    at = lambda i: ctypes.c_void_p(0x10000 * i)  # noqa: E731
+    d = cross_desc()
+    for same in (1, 2, 3):
+        assert fwd(lib, d, q=at(1), k=at(2), v=at(3), o=at(same)) == INVALID
+    names = ("o", "dout", "dq", "dk", "dv")
+    for a, b in (("dq", "o"), ("dk", "dout"), ("dv", "dq"), ("dk", "dq"), ("dv", "dk")):
+        p = {x: at(4 + i) for i, x in enumerate(names)}
+        p[a] = p[b]
+        assert bwd(lib, d, lse=at(2), **p) == INVALID
+    assert bwd(lib, d, o=at(4), dout=at(5), dq=at(6), dk=FAKE, dv=at(7)) == INVALID  # dk over k
+
+    def two(x, y, ys=None):
+        s = dense(1, 2, 24, 64)
+        desc = SquadRotaryDesc(1, 64, 2, 3, 4, 24, 20, 20, sq.SQUAD_BF16, 0, 0)
+        return lib.squad_rotary(ctypes.byref(desc), 2, (ctypes.c_int * 2)(2, 2), (ctypes.c_void_p * 2)(*x),
+                                (SquadStrides * 2)(s, s), (ctypes.c_void_p * 2)(*y), (SquadStrides * 2)(ys or s, s),
+                                FAKE, None)
+
+    a, b, c = 0x20000, 0x30000, 0x40000
+    assert two((a, b), (b, a)) == INVALID and two((a, b), (c, c)) == INVALID and two((a, a), (a, a)) == INVALID
+    assert two((a, b), (a, c), dense(1, 3, 30, 64)) == INVALID  # in place with other strides
