@@ -7,10 +7,11 @@
 // key tile and walks the queries of its head group (dK, dV). S and dP are computed in both:
 // 7 products of 2 n m d flops in place of the 5 of a single kernel, whose dQ parts (one fp32
 // [n, d] per 128 keys) would have to be added in memory: at m = 512 four times the bytes of dQ
-// in fp32 through L2, more than the two products cost.
+// in fp32 through L2, more than the two products cost. (With one key block there would be no parts: not
+// tried as a kernel of its own.)
 //
-// Measured at 27,280 x 512, 24 heads of 128: dQ 250 us, dK and dV 268 us and 15 to join their
-// parts (tensor pipe 54% and 68% busy); together 1,130 TFLOP/s of
+// Measured at 27,280 x 512, 24 heads of 128, under ncu: dQ 250 us, dK and dV 268 us and 15 to join their
+// parts (tensor pipe 54% and 68% busy; replayed back to back 530 in all); together 1,130 TFLOP/s of
 // the seven products, 800 of the five.
 //
 // Rounding: P and dS to bf16 before the products that read them (the tensor core's operand

@@ -8,7 +8,8 @@
 // four passes, shared addresses or not), so a thread always holds 4 x 4 scores (8 loads for 64
 // FMAs) or 4 rows of results: the 256 threads are 4 R groups of rows x 16 of columns (or
 // channels) x S = 4 / R parts of the sum, along the channels for scores and along the 64 for
-// results. The parts of a score are joined by shuffles, those of a result once at the end.
+// results. The parts of a score are joined by shuffles, those of a result once at the end. (8 x 8
+// scores would halve the loads for each FMA; not tried.)
 // The loads of a tile are not covered by the products of the one before, but by another block's.
 // Forward, 8 heads of 128, 4,096 x 1,024: 703 us with R = 1, 562 with 2 (31 TFLOP/s; the
 // shared-memory passes take 0.4 ms of it); 1,000 x 130, 4 heads of 96: 23 and 23 us.

@@ -25,8 +25,9 @@
 // 232 us against 196 us at 27,280 x 512.)
 // A block of 128 x 128 costs the tensor core 4 x 128 x 128 x D flops (1,024 cycles at D = 128)
 // and the multi-function unit 128 x 128 exponentials (1,024 cycles at 16 a cycle): both are
-// near their limit at once. Measured at 27,280 x 512, 24 heads of 128: 158 us, 1,090 TFLOP/s of the
-// 1,634 that a library product reaches alone; tensor pipe 52% and multi-function unit 56% busy. What
+// near their limit at once. Measured at 27,280 x 512, 24 heads of 128: 158 us replayed back to back (1,090
+// TFLOP/s of the 1,634 that a library product reaches alone), 176 to 187 a call with the L2 flushed;
+// tensor pipe 52% and multi-function unit 56% busy. What
 // is left is the chain of one block, wait for S, maximum, exponentials, hand P over, which two
 // jobs an SM cover only in part; a third does not fit TMEM (S and O of a job take 256 columns).
 // A mask of each key is one more product, 0 or -inf times a column of ones on top of S: selects in
