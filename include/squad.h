@@ -339,7 +339,8 @@ squad_status squad_rotary(const squad_rotary_desc* desc, int ntensors, const int
  * No two rows of an output overlap (SQUAD_ERR_ALIGN), nor an output and another or an input
  * (SQUAD_ERR_INVALID_ARG where they begin at the same element).
  * Limits (SQUAD_ERR_UNSUPPORTED): bf16 d in {64, 128}; f32 d a multiple of 32,
- * d <= 256; B and heads <= 65535. */
+ * d <= 256; B and heads <= 65535. B*heads*n and B*kv_heads*m are below 2^31, broadcast
+ * or not (SQUAD_ERR_SHAPE). */
 typedef struct {
   int B, heads, kv_heads, n, m, d;
   int dtype;                        /* squad_dtype */
