@@ -20,19 +20,13 @@
 
 namespace {
 
+using sq::align256;
 using sq::aligned16;
-
-#define SQ_CUDA(call)                                             \
-  do {                                                            \
-    cudaError_t e_ = (call);                                      \
-    if (e_ != cudaSuccess) return sq::host_cuda_fail(int(e_));    \
-  } while (0)
 
 constexpr long long kMaxRows = 1ll << 31;
 constexpr int kMaxGridYZ = 65535;
 
 size_t elem_size(int dtype) { return dtype == SQUAD_BF16 ? 2 : 4; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Strides a tensor of extents B x h x n may have: multiples of 16 bytes and not negative;
 // rows at least d apart; a stride of an extent of 1 is not looked at. broadcast (inputs): batch and

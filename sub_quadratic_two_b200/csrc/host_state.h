@@ -8,6 +8,13 @@
 
 #include "squad.h"
 
+// Returns SQUAD_ERR_CUDA from the calling function where a CUDA call fails.
+#define SQ_CUDA(call)                                          \
+  do {                                                         \
+    cudaError_t e_ = (call);                                   \
+    if (e_ != cudaSuccess) return sq::host_cuda_fail(int(e_)); \
+  } while (0)
+
 #define SQ_HIDDEN __attribute__((visibility("hidden")))
 
 namespace sq {
@@ -29,6 +36,7 @@ SQ_HIDDEN squad_status host_cuda_fail(int code);
 SQ_HIDDEN squad_status host_encode_bf16(CUtensorMap* m, int device, int rank, const void* base,
                                         const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace sq

@@ -41,12 +41,6 @@ squad_status cuda_fail(int code) {
   return SQUAD_ERR_CUDA;
 }
 
-#define SQ_CUDA(call)                                   \
-  do {                                                  \
-    cudaError_t e_ = (call);                            \
-    if (e_ != cudaSuccess) return cuda_fail(int(e_));   \
-  } while (0)
-
 // ---------------------------------------------------------------- per-device state
 
 struct DeviceState {
@@ -103,6 +97,7 @@ struct Plan {
   float scale;
 };
 
+using sq::align256;
 using sq::aligned16;
 
 // with_passes = false checks the tensors only (the k-pass entry points plan their own passes)
@@ -134,8 +129,6 @@ squad_status make_plan(const squad_desc* d, Plan* p, bool with_passes = true) {
   p->scale = d->scale > 0.f ? d->scale : 1.0f / std::sqrt(float(d->d));
   return SQUAD_OK;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Forward workspace: [local-pass output, only when the caller passes no o1][per-head counters].
 size_t fwd_o1_bytes(const Plan& p, const squad_desc* d) { return align256(p.rows * d->d * p.elem); }
