@@ -26,3 +26,10 @@ def test_read_traffic_needs_a_matching_hash(tmp_path):
     other = tmp_path / "k.cuh"
     other.write_text("__global__ void k() {}\n")
     assert bench.read_traffic("fused", [str(other)]) is None
+
+
+def test_recorded_traffic_is_of_the_sources_in_the_tree():
+    # a change of a kernel source asks for a new capture: without one bench.py reports no traffic
+    src = [os.path.join(ROOT, "sub_quadratic_two_b200", "csrc", f) for f in bench.FWD_KERNEL_SOURCES]
+    for launch in ("fused", "pass1", "pass2"):
+        assert bench.read_traffic(launch, src) is not None
